@@ -56,7 +56,9 @@ typedef enum {
     MOE_ERR_DEVICE = 4
 } moe_status;
 
-typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1 } moe_dtype;
+/* MOE_DTYPE_F16 is a type of the unquantised products (moe_linear_t) and of
+ * moe_combine only; the quantised layer and the router projection refuse it. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
 
 /* Storage of the down projection (see moe_layer_t and moe_pack_down). */
 typedef enum { MOE_DOWN_ROWS = 0, MOE_DOWN_COLS = 1 } moe_down_layout;
@@ -374,6 +376,136 @@ moe_status moe_pack_down(const moe_layer_t *layer, uint32_t *dst_q, uint16_t *ds
 /* Host-only check of a layer descriptor (no device access):
  * MOE_OK, MOE_ERR_INVALID_ARG or MOE_ERR_UNSUPPORTED. */
 moe_status moe_layer_check(const moe_layer_t *layer);
+
+/* ------------------------------------------------- unquantised products
+ *
+ * The layers beside the 4-bit experts: a shared expert or a dense projection
+ * kept in bf16 or fp16, experts that are not quantised at all, and a
+ * model's small fp32 layers.  moe_matmul is one product with its epilogue,
+ * moe_grouped_matmul the same product per expert over a planned batch, and
+ * moe_combine the weighted sum over k per token that follows it.  An
+ * unquantised expert block is moe_route_plan, two moe_grouped_matmul calls
+ * (gated gate+up, then down into fp32 rows) and moe_combine, the same
+ * three-part split of router, expert products and combine as the quantised
+ * block (page "perf(moe): attribute the MoE decode gap at the M = 1 expert
+ * gather", Proposed Solution step 2).
+ */
+
+/* f of the epilogue; z is the fp32 sum x.w plus bias. */
+typedef enum {
+    MOE_FN_NONE = 0,
+    MOE_FN_RELU = 1,      /* max(z, 0), NaN kept */
+    MOE_FN_SILU = 2,      /* z / (1 + exp(-z)) */
+    MOE_FN_GELU = 3,      /* z Phi(z), Phi the normal distribution function */
+    MOE_FN_GELU_TANH = 4  /* 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+} moe_fn;
+
+/* How moe_grouped_matmul finds the rows of x and out for the i-th entry of
+ * the plan's sorted_slots, slot s = sorted_slots[i]. */
+typedef enum {
+    MOE_ROWS_TOKEN = 0, /* x row s / top_k (one per token), out row s */
+    MOE_ROWS_SLOT = 1,  /* x row s, out row s */
+    MOE_ROWS_SORTED = 2 /* x row i, out row i: rows already grouped by expert */
+} moe_rows;
+
+/*
+ * Weights of a product, in host memory, its pointers device pointers:
+ *   w        [n_groups][out_features][in_features], dtype
+ *   w_up     NULL, or a second stack of the same layout: the product is
+ *            then gated, out = f(z) * z_up
+ *   bias     NULL, or [n_groups][out_features], dtype, added to z
+ *   bias_up  the same for z_up: given exactly when bias and w_up are
+ * Strides are in elements; 0 means packed.  Rows of w (and w_up) lie
+ * row_stride apart, matrices group_stride, rows of bias (and bias_up)
+ * bias_stride, so gate and up may be the two halves of one stack.
+ * clamp_limit (0 = none) clips z and z_up to [-L, L] before f, NaN kept.
+ * Any in_features and out_features >= 1 are supported.  Pointers and strides
+ * need the alignment of one element; when every base address and row is
+ * 16-byte aligned and in_features fills whole 16-byte chunks, faster loads
+ * are used.  MOE_ERR_UNSUPPORTED for rows of 16 MiB and more.
+ */
+typedef struct {
+    int32_t in_features, out_features;
+    int32_t n_groups;     /* 1 for moe_matmul; experts, 1..MOE_MAX_EXPERTS */
+    int32_t dtype;        /* moe_dtype of x, w and bias */
+    int32_t out_dtype;    /* moe_dtype of out */
+    int32_t fn;           /* moe_fn */
+    float clamp_limit;    /* >= 0; 0 = none */
+    int32_t reserved;     /* 0 */
+    const void *w, *w_up;
+    const void *bias, *bias_up;
+    int64_t row_stride, group_stride, bias_stride;
+} moe_linear_t;
+
+/* Host-only check of a descriptor (no device access). */
+moe_status moe_linear_check(const moe_linear_t *linear);
+
+/* Bytes of device workspace the products need for up to max_rows rows (or
+ * slots); 0 when none is needed (workspace may then be NULL) or the
+ * descriptor is invalid. */
+size_t moe_matmul_workspace_size(const moe_linear_t *linear, int32_t max_rows);
+size_t moe_grouped_workspace_size(const moe_linear_t *linear, int32_t max_slots);
+
+/*
+ * out[r] = residual[r] + f(x[r] w^T + bias)        (f(z) * z_up when gated)
+ *   x         [n_rows][in_features], rows x_stride elements apart
+ *   residual  NULL, or [n_rows][out_features] of residual_dtype, rows
+ *             residual_stride apart
+ *   out       [n_rows][out_features], rows out_stride apart
+ *   workspace moe_matmul_workspace_size(linear, n_rows) bytes, 256-byte
+ *             aligned; contents need no initialisation.  Calls that may
+ *             overlap in time need a workspace each.
+ * Strides of 0 mean packed rows.  fp32 products and sums throughout (bf16
+ * and fp16 products are exact), one rounding to out_dtype at the store.
+ * Repeated calls are bitwise equal; which kernel runs, and with it the order
+ * of the fp32 sums, depends on the shapes, strides and alignments only.
+ * out may be residual itself (same type and stride); it must not overlap
+ * anything else.  n_groups must be 1.  n_rows == 0 launches nothing.
+ */
+moe_status moe_matmul(const moe_linear_t *linear, const void *x, int64_t x_stride, int32_t n_rows,
+                      const void *residual, int32_t residual_dtype, int64_t residual_stride, void *out,
+                      int64_t out_stride, void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * The same product for every expert of a planned batch, each over its own
+ * rows: for every distinct expert e and every slot the plan lists for it,
+ *   out[row] = f(x[row'] w[e]^T + bias[e])
+ * with row and row' as `rows` (moe_rows) says.
+ *   plan      of n_slots slots over n_groups experts (moe_expert_plan,
+ *             moe_route_plan); work and sorted_slots are read
+ *             (MOE_ROWS_SORTED: work only)
+ *   top_k     slots per token, >= 1; used by MOE_ROWS_TOKEN
+ *   x         [n_slots / top_k rounded up] (token) or [n_slots] rows
+ *   out       [n_slots] rows
+ * Rows that no expert lists (slots the planner left out for a bad expert id)
+ * are left as they were.  Each distinct expert's weights are read once per
+ * row tile; no host synchronisation: the grid covers the largest number of
+ * tiles that n_slots slots can need.  Records or slots outside the plan's
+ * range are skipped, so a malformed plan never reads or writes out of bounds.
+ * n_slots == 0 launches nothing.  Otherwise as moe_matmul.
+ */
+moe_status moe_grouped_matmul(const moe_linear_t *linear, const void *x, int64_t x_stride, int32_t n_slots,
+                              int32_t top_k, int32_t rows, const moe_plan_t *plan, void *out, int64_t out_stride,
+                              void *workspace, size_t workspace_bytes, void *hip_stream);
+
+/*
+ * out[t] = residual[t] + sum_{j < top_k} topk_w[t][j] * y[t * top_k + j]
+ *   y         [n_tokens * top_k][hidden] of y_dtype, packed (the rows that
+ *             moe_grouped_matmul writes by slot)
+ *   topk_idx  int32 [n_tokens][top_k]: a token with an id outside
+ *             0 .. n_experts-1 becomes NaN and its y rows count for nothing
+ *   topk_w    fp32 [n_tokens][top_k]
+ *   residual  NULL, or [n_tokens][hidden] of residual_dtype, packed
+ *   out       [n_tokens][hidden] of out_dtype, packed; may be residual itself
+ *             (same type), must not overlap anything else
+ * fp32 sums in j order, the residual added last, one rounding ("f32 partials
+ * with a single final rounding", page "perf(moe): batched decode scales 1.55x
+ * against 3.25x on dense", Implementation Notes).  Types are any moe_dtype.
+ */
+moe_status moe_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx, const float *topk_w,
+                       int32_t n_tokens, int32_t hidden, int32_t top_k, int32_t n_experts,
+                       const void *residual, int32_t residual_dtype, void *out, int32_t out_dtype,
+                       void *hip_stream);
 
 /* Static description of a status code. */
 const char *moe_status_str(moe_status status);

@@ -18,10 +18,16 @@ import torch
 from . import build as _build
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = range(5)
-MOE_DTYPE_F32, MOE_DTYPE_BF16 = 0, 1
+MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
 MOE_DOWN_ROWS, MOE_DOWN_COLS = 0, 1
 MOE_ACT_SWIGLU, MOE_ACT_GEGLU = 0, 1
 _ACTIVATIONS = {"swiglu": MOE_ACT_SWIGLU, "geglu": MOE_ACT_GEGLU}
+MOE_FN_NONE, MOE_FN_RELU, MOE_FN_SILU, MOE_FN_GELU, MOE_FN_GELU_TANH = range(5)
+_FNS = {"none": MOE_FN_NONE, "relu": MOE_FN_RELU, "silu": MOE_FN_SILU, "gelu": MOE_FN_GELU,
+        "gelu_tanh": MOE_FN_GELU_TANH}
+MOE_ROWS_TOKEN, MOE_ROWS_SLOT, MOE_ROWS_SORTED = range(3)
+_ROWS = {"token": MOE_ROWS_TOKEN, "slot": MOE_ROWS_SLOT, "sorted": MOE_ROWS_SORTED}
+_DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
 MOE_MAX_EXPERTS = 1024
 MOE_MAX_TOP_K = 16
 MOE_MAX_TOKENS = 65535
@@ -53,12 +59,23 @@ class PlanStruct(C.Structure):
                 ("unique_experts", C.c_void_p), ("n_unique", C.c_void_p), ("work", C.c_void_p)]
 
 
+class LinearStruct(C.Structure):
+    _fields_ = [
+        ("in_features", C.c_int32), ("out_features", C.c_int32), ("n_groups", C.c_int32), ("dtype", C.c_int32),
+        ("out_dtype", C.c_int32), ("fn", C.c_int32), ("clamp_limit", C.c_float), ("reserved", C.c_int32),
+        ("w", C.c_void_p), ("w_up", C.c_void_p), ("bias", C.c_void_p), ("bias_up", C.c_void_p),
+        ("row_stride", C.c_int64), ("group_stride", C.c_int64), ("bias_stride", C.c_int64),
+    ]
+
+
 _lib = None
 
 EXPORTS = ("moe_router_logits", "moe_route_topk", "moe_expert_plan", "moe_route_plan", "moe_workspace_size",
            "moe_decode_step", "moe_decode_step_residual",
            "moe_decode_layer", "moe_decode_layer_static", "moe_route_gate_up", "moe_expert_gate_up", "moe_expert_down_combine", "moe_pack_down",
-           "moe_layer_check", "moe_status_str", "moe_abi_version")
+           "moe_layer_check", "moe_status_str", "moe_abi_version",
+           "moe_linear_check", "moe_matmul_workspace_size", "moe_grouped_workspace_size", "moe_matmul",
+           "moe_grouped_matmul", "moe_combine")
 
 
 def library_path() -> str:
@@ -111,6 +128,20 @@ def lib() -> C.CDLL:
         L.moe_pack_down.restype = C.c_int
         L.moe_layer_check.argtypes = [C.POINTER(LayerStruct)]
         L.moe_layer_check.restype = C.c_int
+        i64, lp = C.c_int64, C.POINTER(LinearStruct)
+        L.moe_linear_check.argtypes = [lp]
+        L.moe_linear_check.restype = C.c_int
+        L.moe_matmul_workspace_size.argtypes = [lp, i32]
+        L.moe_matmul_workspace_size.restype = C.c_size_t
+        L.moe_grouped_workspace_size.argtypes = [lp, i32]
+        L.moe_grouped_workspace_size.restype = C.c_size_t
+        L.moe_matmul.argtypes = [lp, vp, i64, i32, vp, i32, i64, vp, i64, vp, C.c_size_t, vp]
+        L.moe_matmul.restype = C.c_int
+        L.moe_grouped_matmul.argtypes = [lp, vp, i64, i32, i32, i32, C.POINTER(PlanStruct), vp, i64, vp, C.c_size_t,
+                                         vp]
+        L.moe_grouped_matmul.restype = C.c_int
+        L.moe_combine.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp, i32, vp]
+        L.moe_combine.restype = C.c_int
         L.moe_status_str.argtypes = [C.c_int]
         L.moe_status_str.restype = C.c_char_p
         L.moe_abi_version.argtypes = []
@@ -503,3 +534,253 @@ def decode_layer_static(layer: DeviceLayer, x: torch.Tensor, logits: torch.Tenso
                                          C.byref(plan.struct), _ptr(residual), _ptr(out), _stream(stream)),
            "moe_decode_layer_static")
     return out
+
+
+# --------------------------------------------------- unquantised products
+# These run on the current stream of the tensors' own device (or on `stream`),
+# whichever device is current, and what they allocate belongs to that stream.
+# They sit on the path of every decoded token, so a call that needs no
+# switch of device or stream makes none.
+@dataclass
+class Linear:
+    """Weights of a product plus the ABI descriptor (moe_linear_t) pointing at them."""
+
+    w: torch.Tensor
+    w_up: Optional[torch.Tensor]
+    bias: Optional[torch.Tensor]
+    bias_up: Optional[torch.Tensor]
+    in_features: int
+    out_features: int
+    n_groups: int
+    out_dtype: torch.dtype
+    struct: LinearStruct
+
+    @staticmethod
+    def from_tensors(w: torch.Tensor, bias: Optional[torch.Tensor] = None, w_up: Optional[torch.Tensor] = None,
+                     bias_up: Optional[torch.Tensor] = None, activation: str = "none",
+                     out_dtype: Optional[torch.dtype] = None, clamp_limit: float = 0.0) -> "Linear":
+        """``w``: [out, in], or [experts, out, in] for grouped_matmul, bf16, fp16 or fp32, each
+        row contiguous; ``w_up`` (same shape and strides) makes the product gated.  ``bias`` and
+        ``bias_up``: [out] or [experts, out].  ``activation``: none, relu, silu, gelu or
+        gelu_tanh.  ``out_dtype`` defaults to the weights' type.  The tensors are used in place
+        and kept alive by this object."""
+        if activation not in _FNS:
+            raise ValueError(f"activation must be one of {sorted(_FNS)}")
+        if w is None or w.dim() not in (2, 3) or w.dtype not in _DTYPES or not w.is_cuda or w.numel() == 0:
+            raise ValueError("w must be a non-empty [out, in] or [experts, out, in] bf16, fp16 or fp32 device tensor")
+        out_dtype = w.dtype if out_dtype is None else out_dtype
+        if out_dtype not in _DTYPES:
+            raise ValueError("out_dtype must be bf16, fp16 or fp32")
+        if (bias_up is not None) != (bias is not None and w_up is not None):
+            raise ValueError("bias_up goes with bias and w_up")
+        N, K = w.shape[-2:]
+        E = w.shape[0] if w.dim() == 3 else 1
+        if K > 1 and w.stride(-1) != 1:
+            raise ValueError("the rows of w must be contiguous")
+        if w_up is not None and (w_up.shape != w.shape or w_up.dtype != w.dtype or w_up.device != w.device
+                                 or any(n > 1 and a != b for n, a, b in zip(w.shape, w.stride(), w_up.stride()))):
+            raise ValueError("w_up must match w in shape, type, device and strides")
+        for b in (bias, bias_up):
+            if b is None:
+                continue
+            if b.shape != w.shape[:-1] or b.dtype != w.dtype or b.device != w.device or (N > 1 and b.stride(-1) != 1):
+                raise ValueError("a bias must be [out] or [experts, out] of w's type and device, rows contiguous")
+            if b.dim() == 2 and E > 1 and b.stride(0) != bias.stride(0):
+                raise ValueError("bias and bias_up must have the same strides")
+        row = w.stride(-2) if N > 1 else K
+        group = w.stride(0) if E > 1 else 0
+        bias_group = bias.stride(0) if bias is not None and E > 1 else 0
+        if row < K or (E > 1 and group <= 0) or (bias is not None and E > 1 and bias_group <= 0):
+            raise ValueError("expanded (broadcast) weights have no layout here")
+        st = LinearStruct(in_features=K, out_features=N, n_groups=E, dtype=_DTYPES[w.dtype],
+                          out_dtype=_DTYPES[out_dtype], fn=_FNS[activation], clamp_limit=float(clamp_limit),
+                          w=w.data_ptr(), w_up=None if w_up is None else w_up.data_ptr(),
+                          bias=None if bias is None else bias.data_ptr(),
+                          bias_up=None if bias_up is None else bias_up.data_ptr(),
+                          row_stride=row, group_stride=group, bias_stride=bias_group)
+        lin = Linear(w, w_up, bias, bias_up, K, N, E, out_dtype, st)
+        _check(lin.check(), "moe_linear_check")
+        return lin
+
+    def check(self) -> int:
+        return lib().moe_linear_check(C.byref(self.struct))
+
+
+def matmul_workspace_size(linear: Linear, max_rows: int) -> int:
+    return int(lib().moe_matmul_workspace_size(C.byref(linear.struct), int(max_rows)))
+
+
+def grouped_workspace_size(linear: Linear, max_slots: int) -> int:
+    return int(lib().moe_grouped_workspace_size(C.byref(linear.struct), int(max_slots)))
+
+
+def _alloc_bytes(n: int, device) -> Optional[torch.Tensor]:
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def alloc_matmul_workspace(linear: Linear, max_rows: int) -> Optional[torch.Tensor]:
+    """The workspace matmul needs for up to max_rows rows; None when it needs none."""
+    return _alloc_bytes(matmul_workspace_size(linear, max_rows), linear.w.device)
+
+
+def alloc_grouped_workspace(linear: Linear, max_slots: int) -> Optional[torch.Tensor]:
+    """The workspace grouped_matmul needs for up to max_slots slots; None when it needs none."""
+    return _alloc_bytes(grouped_workspace_size(linear, max_slots), linear.w.device)
+
+
+def _on(device: torch.device, stream, call):
+    """call(stream handle) with `device` current and `stream` (default: that device's
+    current one) the stream that allocations belong to."""
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return call(torch._C._cuda_getCurrentRawStream(device.index))
+        with torch.cuda.device(device):
+            return call(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between the rows of a 2-D tensor with contiguous rows, 0 when it has one row."""
+    rows, cols = t.shape
+    s0, s1 = t.stride()
+    if cols > 1 and s1 != 1:
+        raise ValueError(f"the rows of {name} must be contiguous")
+    if rows <= 1:
+        return 0
+    if s0 < cols:
+        raise ValueError(f"the rows of {name} overlap (an expanded tensor?)")
+    return s0
+
+
+def _out_2d(out: Optional[torch.Tensor], rows: int, cols: int, dtype, device) -> torch.Tensor:
+    if out is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device)
+    if out.dtype != dtype or out.shape != (rows, cols) or out.device != device:
+        raise ValueError(f"out must be a {dtype} [{rows}, {cols}] tensor on {device}, "
+                         f"got {out.dtype} {tuple(out.shape)} on {out.device}")
+    return out
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, device):
+    """(pointer, bytes) of the caller's workspace, or of one allocated here for the call;
+    the tensor comes back too, to live until the call is enqueued."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _check_product_x(linear: Linear, x: torch.Tensor):
+    w = linear.w
+    if x.dim() != 2 or x.dtype != w.dtype or x.device != w.device or x.shape[1] != linear.in_features:
+        raise ValueError(f"x must be a {w.dtype} [rows, {linear.in_features}] tensor on {w.device}, "
+                         f"got {x.dtype} {tuple(x.shape)} on {x.device}")
+
+
+def matmul(linear: Linear, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_matmul: x [rows, in] -> out [rows, out] = residual + f(x w^T + bias), f gated when the
+    linear has w_up.  Rows of x, residual and out may be strided; residual is any of the three
+    types; out may be residual itself."""
+    _check_product_x(linear, x)
+    device, rows = x.device, x.shape[0]
+    xs = _row_stride(x, "x")
+    res = res_type = res_stride = 0
+    if residual is not None:
+        if residual.shape != (rows, linear.out_features) or residual.device != device or residual.dtype not in _DTYPES:
+            raise ValueError(f"residual must be a [{rows}, {linear.out_features}] bf16, fp16 or fp32 tensor on {device}")
+        res, res_type = residual.data_ptr(), _DTYPES[residual.dtype]
+        res_stride = _row_stride(residual, "residual")
+
+    def call(handle):
+        o = _out_2d(out, rows, linear.out_features, linear.out_dtype, device)
+        need = 0 if workspace is not None else matmul_workspace_size(linear, rows)
+        wp, wb, keep = _workspace(workspace, need, device)
+        _check(lib().moe_matmul(C.byref(linear.struct), x.data_ptr(), xs, rows, res or None, res_type, res_stride,
+                                o.data_ptr(), _row_stride(o, "out"), wp, wb, handle), "moe_matmul")
+        return o
+
+    return _on(device, stream, call)
+
+
+def grouped_matmul(linear: Linear, x: torch.Tensor, plan: Plan, n_slots: int, top_k: int = 1, rows: str = "token",
+                   out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """moe_grouped_matmul over a plan of n_slots slots: out [n_slots, out].  ``rows``: "token" (x has a
+    row per token, slot s reads row s // top_k), "slot" (x has a row per slot) or "sorted"
+    (rows of x and out lie grouped by expert, in the plan's order).  Rows of slots that the
+    plan does not list are left as they are (unset when out is allocated here)."""
+    if rows not in _ROWS:
+        raise ValueError(f"rows must be one of {sorted(_ROWS)}")
+    _check_product_x(linear, x)
+    device, mode, n_slots, top_k = x.device, _ROWS[rows], int(n_slots), int(top_k)
+    if n_slots < 0 or top_k < 1:
+        raise ValueError("n_slots must be at least 0 and top_k at least 1")
+    if x.shape[0] != (-(-n_slots // top_k) if mode == MOE_ROWS_TOKEN else n_slots):
+        raise ValueError(f"x has {x.shape[0]} rows, which does not fit {n_slots} slots with rows={rows!r}, top_k={top_k}")
+    work, slots = plan.work, plan.sorted_slots
+    if work.numel() < 4 * min(linear.n_groups, max(n_slots, 1)) or work.device != device:
+        raise ValueError(f"the plan's records are too few for {linear.n_groups} experts or not on {device}")
+    if mode != MOE_ROWS_SORTED and (slots.numel() < n_slots or slots.device != device):
+        raise ValueError(f"the plan's sorted_slots are fewer than {n_slots} or not on {device}")
+    xs = _row_stride(x, "x")
+
+    def call(handle):
+        o = _out_2d(out, n_slots, linear.out_features, linear.out_dtype, device)
+        need = 0 if workspace is not None else grouped_workspace_size(linear, n_slots)
+        wp, wb, keep = _workspace(workspace, need, device)
+        _check(lib().moe_grouped_matmul(C.byref(linear.struct), x.data_ptr(), xs, n_slots, top_k, mode,
+                                        C.byref(plan.struct), o.data_ptr(), _row_stride(o, "out"), wp, wb, handle),
+               "moe_grouped_matmul")
+        return o
+
+    return _on(device, stream, call)
+
+
+def combine(y: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, n_experts: int,
+            residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """moe_combine: y [B * k, H], idx int32 [B, k], w fp32 [B, k] -> out [B, H] =
+    residual + the weighted sum of each token's k rows.  out_dtype defaults to out's type, else
+    the residual's, else y's."""
+    if y.dim() != 2 or y.dtype not in _DTYPES or not y.is_contiguous() or not y.is_cuda:
+        raise ValueError("y must be a contiguous bf16, fp16 or fp32 [slots, hidden] device tensor")
+    device, H = y.device, y.shape[1]
+    if idx.dim() != 2 or idx.dtype != torch.int32 or not idx.is_contiguous() or idx.device != device:
+        raise ValueError(f"idx must be a contiguous int32 [B, k] tensor on {device}")
+    B, k = idx.shape
+    if w.dtype != torch.float32 or w.shape != idx.shape or not w.is_contiguous() or w.device != device:
+        raise ValueError(f"w must be a contiguous fp32 [{B}, {k}] tensor on {device}")
+    if y.shape[0] != B * k:
+        raise ValueError(f"y has {y.shape[0]} rows, {B * k} needed for {B} tokens of {k} slots")
+    res = res_type = 0
+    if residual is not None:
+        if (residual.shape != (B, H) or residual.device != device or residual.dtype not in _DTYPES
+                or not residual.is_contiguous()):
+            raise ValueError(f"residual must be a contiguous [{B}, {H}] bf16, fp16 or fp32 tensor on {device}")
+        res, res_type = residual.data_ptr(), _DTYPES[residual.dtype]
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        out_dtype = out.dtype
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+    elif out_dtype is None:
+        out_dtype = y.dtype if residual is None else residual.dtype
+    if out_dtype not in _DTYPES:
+        raise ValueError("out must be bf16, fp16 or fp32")
+
+    def call(handle):
+        o = _out_2d(out, B, H, out_dtype, device)
+        _check(lib().moe_combine(y.data_ptr(), _DTYPES[y.dtype], idx.data_ptr(), w.data_ptr(), B, H, k,
+                                 int(n_experts), res or None, res_type, o.data_ptr(), _DTYPES[out_dtype], handle),
+               "moe_combine")
+        return o
+
+    return _on(device, stream, call)

@@ -1,0 +1,89 @@
+// Weighted sum over the k rows of a token (gfx950) and moe_combine: the
+// combine of an expert block whose products wrote one row per slot ("sum over
+// k per token": page "perf(moe): batched decode scales 1.55x against 3.25x on
+// dense", Proposed Solution).
+//
+// out[t][c] = residual[t][c] + sum_j w[t][j] y[t k + j][c], fp32 fused
+// multiply-adds in j order.  Memory-bound: y is read once.  A thread takes four
+// columns of a token, one 16-byte access per fp32 row, four rows' loads
+// issued together.
+#include <hip/hip_runtime.h>
+
+#include "matmul_device.h"
+#include "matmul_internal.h"
+
+namespace moe {
+
+constexpr int kCombineCols = 4;
+
+struct CombineArgs {
+    const void *y;
+    const int *idx;
+    const float *w;
+    const void *residual;
+    void *out;
+    int y_dtype, res_dtype, out_dtype;
+    int n_tokens, hidden, top_k, n_experts;
+    int groups;  // column groups of a token
+    int vec;     // four columns are one aligned access everywhere
+};
+
+__global__ __launch_bounds__(256) void combine_rows_kernel(CombineArgs a) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int t = (int)(i / a.groups);
+    if (t >= a.n_tokens) return;
+    const int c = (int)(i - (int64_t)t * a.groups) * kCombineCols;
+    const int64_t s0 = (int64_t)t * a.top_k;
+    mm_f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    bool bad = false;
+    auto row = [&](int j) -> mm_f32x4 {
+        const int64_t at = (s0 + j) * a.hidden + c;
+        if (a.vec) return load_value4(a.y, at, a.y_dtype);
+        mm_f32x4 v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (c + q < a.hidden) v[q] = load_value(a.y, at + q, a.y_dtype);
+        return v;
+    };
+    auto add = [&](int j, const mm_f32x4 &v) {
+        const float w = a.w[s0 + j];
+        bad |= (unsigned)a.idx[s0 + j] >= (unsigned)a.n_experts;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[q] = fmaf(w, v[q], acc[q]);
+    };
+    int j = 0;
+    for (; j + 4 <= a.top_k; j += 4) {
+        const mm_f32x4 v0 = row(j), v1 = row(j + 1), v2 = row(j + 2), v3 = row(j + 3);
+        add(j, v0);
+        add(j + 1, v1);
+        add(j + 2, v2);
+        add(j + 3, v3);
+    }
+    for (; j < a.top_k; ++j) add(j, row(j));
+    if (bad) acc = mm_f32x4{} + __builtin_nanf("");
+    store4(a.out, (int64_t)t * a.hidden, a.out_dtype, a.residual, (int64_t)t * a.hidden, a.res_dtype, a.vec, c,
+           a.hidden, acc);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx, const float *topk_w,
+                                  int32_t n_tokens, int32_t hidden, int32_t top_k, int32_t n_experts,
+                                  const void *residual, int32_t residual_dtype, void *out, int32_t out_dtype,
+                                  void *hip_stream) {
+    const moe_status st = check_combine(y, y_dtype, topk_idx, topk_w, n_tokens, hidden, top_k, n_experts, residual,
+                                        residual_dtype, out, out_dtype);
+    if (st != MOE_OK || n_tokens == 0) return st;
+    const uintptr_t ya = 4 * dtype_size(y_dtype), oa = 4 * dtype_size(out_dtype);
+    const uintptr_t ra = residual ? 4 * dtype_size(residual_dtype) : 1;
+    const bool vec = hidden % kCombineCols == 0 && (uintptr_t)y % ya == 0 && (uintptr_t)out % oa == 0 &&
+                     (uintptr_t)residual % ra == 0;
+    const int groups = (hidden + kCombineCols - 1) / kCombineCols;
+    const CombineArgs a{y, topk_idx, topk_w, residual, out, y_dtype, residual_dtype, out_dtype,
+                        n_tokens, hidden, top_k, n_experts, groups, vec};
+    const unsigned blocks = (unsigned)(((int64_t)groups * n_tokens + 255) / 256);
+    hipLaunchKernelGGL(combine_rows_kernel, dim3(blocks), dim3(256), 0, (hipStream_t)hip_stream, a);
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}

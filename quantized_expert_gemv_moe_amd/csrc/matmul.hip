@@ -1,0 +1,173 @@
+// Unquantised products (gfx950): tile kernels, entry points moe_matmul and
+// moe_grouped_matmul.
+#include <hip/hip_runtime.h>
+
+#include "matmul_device.h"
+#include "matmul_internal.h"
+
+namespace moe {
+
+// 64 x 64 tile through registers and LDS, for rows of any alignment.  Four
+// waves, 2 x 2, each a 32 x 32 corner: 2 x 2 MFMA tiles.  A step covers 128
+// bytes of every row: each thread fetches two chunks of x and two of w for
+// the next step while the current one is multiplied, and puts them into the
+// other half of LDS afterwards.  A row's eight chunks are stored XORed with
+// bits of its row number, so the 16 rows that a quarter wave reads at one chunk
+// number fall into different banks.
+// Gated: half of the 64 rows of w are gate rows, half up rows of the same
+// columns, paired within a wave, so a tile has 32 columns.
+template <int DT, bool GATED, bool ALIGNED>
+__global__ __launch_bounds__(256) void matmul_tile64_kernel(MatmulArgs a) {
+    constexpr int BM = 64, BW = 64, MT = 2, NT = 2;
+    constexpr int NTC = GATED ? NT / 2 : NT;      // column tiles of a wave
+    constexpr int CW = NTC * 16;                  // columns of a wave
+    __shared__ mm_u32x4 lds[2][BM + BW][8];
+    __shared__ int orow[BM];
+    MatmulTile t;
+    if (a.rows_mode == kRowsDense ? !dense_tile<8>(a, BM, &t) : !grouped_tile(a, BM, &t)) return;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
+    const int wm = wave & 1, wn = wave >> 1;
+    const int g = lane >> 4, r16 = lane & 15;
+    const int col0 = t.tile_n * 2 * CW;
+    if (tid < BM) orow[tid] = out_row(a, t, t.row0 + tid);
+    __syncthreads();
+
+    // this thread's chunks: rows tid / 8 and 32 further of either operand
+    const char *xp[2], *wp[2];
+    const int c8 = tid & 7;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int row = tid / 8 + 32 * i;
+        xp[i] = a.x + (int64_t)x_row(a, orow[row]) * a.x_stride;
+        // LDS row of w -> (wave column, tile j, row q of A) -> column: a lane
+        // of D then holds 4 NTC consecutive columns
+        const int j = (row & 31) >> 4, q = row & 15;
+        const int jc = GATED ? 0 : j;
+        int col = col0 + (row >> 5) * CW + (q >> 2) * 4 * NTC + jc * 4 + (q & 3);
+        if (col >= a.N) col = a.N - 1;
+        const char *base = GATED && j ? a.w_up : a.w;
+        wp[i] = base + (int64_t)t.group * a.w_group + (int64_t)col * a.w_row;
+    }
+    mm_u32x4 xr[2], wr[2];
+    auto fetch = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            xr[i] = load_chunk<DT, ALIGNED>(xp[i], c, a.K);
+            wr[i] = load_chunk<DT, ALIGNED>(wp[i], c, a.K);
+        }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int row = tid / 8 + 32 * i;
+            lds[buf][row][c8 ^ ((row >> 1) & 7)] = xr[i];
+            lds[buf][BM + row][c8 ^ ((row >> 1) & 7)] = wr[i];
+        }
+    };
+    mm_f32x4 acc[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[m][n] = mm_f32x4{0.f, 0.f, 0.f, 0.f};
+    const int steps = (a.K + 8 * kChunk<DT> - 1) / (8 * kChunk<DT>);
+    fetch(c8);
+    put(0);
+    __syncthreads();
+    for (int s = 0; s < steps; ++s) {
+        const int buf = s & 1;
+        if (s + 1 < steps) fetch((s + 1) * 8 + c8);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            mm_u32x4 xf[MT], wf[NT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int row = wm * 32 + m * 16 + r16;
+                xf[m] = lds[buf][row][(4 * h + g) ^ ((row >> 1) & 7)];
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int row = wn * 32 + n * 16 + r16;
+                wf[n] = lds[buf][BM + row][(4 * h + g) ^ ((row >> 1) & 7)];
+            }
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[m][n] = mma<DT>(wf[n], xf[m], acc[m][n]);
+        }
+        if (s + 1 < steps) put(buf ^ 1);
+        __syncthreads();
+    }
+
+    const int col = col0 + wn * CW + g * 4 * NTC;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        mm_f32x4 *z = acc[m];
+        if (a.bias) {
+            add_bias<DT, NTC>(z, a.bias + (int64_t)t.group * a.bias_group, col, a.N);
+            if constexpr (GATED) add_bias<DT, NTC>(z + NTC, a.bias_up + (int64_t)t.group * a.bias_group, col, a.N);
+        }
+        clip_all<NT>(z, a.clamp);
+        apply_fn<NTC>(z, a.fn);
+        if constexpr (GATED)
+#pragma unroll
+            for (int n = 0; n < NTC; ++n) z[n] *= z[n + NTC];
+        const int o = orow[wm * 32 + m * 16 + r16];
+        if (o < 0) continue;
+#pragma unroll
+        for (int n = 0; n < NTC; ++n)
+            store4(a.out, (int64_t)o * a.out_stride, a.out_dtype, a.residual, (int64_t)o * a.res_stride, a.res_dtype,
+                   a.vec_out, col + 4 * n, a.N, z[n]);
+    }
+}
+
+template <int DT, bool GATED, bool ALIGNED>
+static void launch_tile64(const MatmulArgs &a, const MatmulChoice &c, hipStream_t s) {
+    const unsigned blocks = (unsigned)(((int64_t)c.tiles_m * c.tiles_n + 7) / 8 * 8);
+    hipLaunchKernelGGL((matmul_tile64_kernel<DT, GATED, ALIGNED>), dim3(blocks), dim3(256), 0, s, a);
+}
+
+template <int DT>
+static void launch_dtype(const MatmulArgs &a, const MatmulChoice &c, hipStream_t s) {
+    if (a.w_up)
+        c.aligned ? launch_tile64<DT, true, true>(a, c, s) : launch_tile64<DT, true, false>(a, c, s);
+    else
+        c.aligned ? launch_tile64<DT, false, true>(a, c, s) : launch_tile64<DT, false, false>(a, c, s);
+}
+
+moe_status launch_matmul(const moe_linear_t *linear, const MatmulArgs &a, const MatmulChoice &c, void *workspace,
+                         hipStream_t s) {
+    (void)workspace;
+    switch (linear->dtype) {
+        case MOE_DTYPE_BF16: launch_dtype<MOE_DTYPE_BF16>(a, c, s); break;
+        case MOE_DTYPE_F16: launch_dtype<MOE_DTYPE_F16>(a, c, s); break;
+        default: launch_dtype<MOE_DTYPE_F32>(a, c, s); break;
+    }
+    return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_matmul(const moe_linear_t *linear, const void *x, int64_t x_stride, int32_t n_rows,
+                                 const void *residual, int32_t residual_dtype, int64_t residual_stride, void *out,
+                                 int64_t out_stride, void *workspace, size_t workspace_bytes, void *hip_stream) {
+    MatmulArgs a;
+    MatmulChoice c;
+    const moe_status st = prepare_matmul(linear, x, x_stride, n_rows, 1, kRowsDense, nullptr, residual, residual_dtype,
+                                         residual_stride, out, out_stride, workspace, workspace_bytes, &a, &c);
+    if (st != MOE_OK || a.rows == 0) return st;
+    return launch_matmul(linear, a, c, workspace, (hipStream_t)hip_stream);
+}
+
+extern "C" moe_status moe_grouped_matmul(const moe_linear_t *linear, const void *x, int64_t x_stride, int32_t n_slots,
+                                         int32_t top_k, int32_t rows, const moe_plan_t *plan, void *out,
+                                         int64_t out_stride, void *workspace, size_t workspace_bytes,
+                                         void *hip_stream) {
+    MatmulArgs a;
+    MatmulChoice c;
+    const moe_status st = prepare_matmul(linear, x, x_stride, n_slots, top_k, rows, plan, nullptr, 0, 0, out,
+                                         out_stride, workspace, workspace_bytes, &a, &c);
+    if (st != MOE_OK || a.rows == 0) return st;
+    return launch_matmul(linear, a, c, workspace, (hipStream_t)hip_stream);
+}

@@ -1,0 +1,238 @@
+// Host-only part of the unquantised products: argument checks, choice of
+// kernel and workspace sizes.  Nothing here touches the device.
+#include <stdint.h>
+
+#include "matmul_internal.h"
+
+namespace moe {
+
+static bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+static bool dtype_ok(int32_t d) { return d == MOE_DTYPE_F32 || d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
+
+// Bytes between rows stay below this, so that the offsets of a tile's rows
+// from its first fit 32 bits.
+constexpr int64_t kMaxRowBytes = 1 << 24;
+constexpr int64_t kMaxGroupElems = (int64_t)1 << 40;
+// Workgroups of one launch: the runtime takes fewer than 2^32 threads.
+constexpr int64_t kMaxBlocks = (int64_t)1 << 22;
+
+bool spans_overlap(const Span &a, const Span &b) {
+    if (a.rows <= 0 || b.rows <= 0 || a.width <= 0 || b.width <= 0) return false;
+    const uint64_t a0 = (uint64_t)(uintptr_t)a.base, b0 = (uint64_t)(uintptr_t)b.base;
+    const uint64_t a1 = a0 + (uint64_t)((a.rows - 1) * a.stride + a.width);
+    const uint64_t b1 = b0 + (uint64_t)((b.rows - 1) * b.stride + b.width);
+    if (a1 <= b0 || b1 <= a0) return false;
+    // columns of one buffer: equal strides, and every row of one lies in the
+    // gaps of the other
+    if (a.stride == b.stride && a.stride > 0) {
+        const uint64_t s = (uint64_t)a.stride;
+        const uint64_t d = b0 >= a0 ? (b0 - a0) % s : (s - (a0 - b0) % s) % s;
+        if (d >= (uint64_t)a.width && d + (uint64_t)b.width <= s) return false;
+    }
+    return true;
+}
+
+static int64_t stride_or(int64_t stride, int64_t packed) { return stride ? stride : packed; }
+
+moe_status check_linear(const moe_linear_t *L) {
+    if (!L) return MOE_ERR_INVALID_ARG;
+    if (L->in_features < 1 || L->out_features < 1 || L->n_groups < 1) return MOE_ERR_INVALID_ARG;
+    if (L->n_groups > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+    if (!dtype_ok(L->dtype) || !dtype_ok(L->out_dtype)) return MOE_ERR_INVALID_ARG;
+    if (L->fn < MOE_FN_NONE || L->fn > MOE_FN_GELU_TANH || L->reserved != 0) return MOE_ERR_INVALID_ARG;
+    if (!(L->clamp_limit >= 0.0f) || L->clamp_limit > 3.0e38f) return MOE_ERR_INVALID_ARG;
+    const size_t es = dtype_size(L->dtype);
+    if (!L->w || (L->bias_up && !L->w_up) || (L->bias_up && !L->bias) || (L->bias && L->w_up && !L->bias_up))
+        return MOE_ERR_INVALID_ARG;
+    const void *ptrs[4] = {L->w, L->w_up, L->bias, L->bias_up};
+    for (const void *p : ptrs)
+        if (p && !aligned(p, es)) return MOE_ERR_INVALID_ARG;
+    if (L->row_stride < 0 || L->group_stride < 0 || L->bias_stride < 0) return MOE_ERR_INVALID_ARG;
+    const int64_t row = stride_or(L->row_stride, L->in_features);
+    if (row < L->in_features) return MOE_ERR_INVALID_ARG;
+    if (row >= kMaxRowBytes / (int64_t)es) return MOE_ERR_UNSUPPORTED;
+    const int64_t mat = (L->out_features - 1) * row + L->in_features;
+    if (L->n_groups > 1) {
+        if (L->group_stride && L->group_stride < mat) return MOE_ERR_INVALID_ARG;
+        if (L->bias && L->bias_stride && L->bias_stride < L->out_features) return MOE_ERR_INVALID_ARG;
+        if (stride_or(L->group_stride, L->out_features * row) > kMaxGroupElems || L->bias_stride > kMaxGroupElems)
+            return MOE_ERR_UNSUPPORTED;
+    }
+    return MOE_OK;
+}
+
+static int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+// Most row tiles of `tile` rows that `rows` slots spread over `groups`
+// groups can need: every group in use may end in a partial tile.
+static int64_t ragged_tiles(int64_t rows, int64_t groups, int64_t tile) {
+    const int64_t used = rows < groups ? rows : groups;
+    return (rows + used * (tile - 1)) / tile;
+}
+
+MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bool is_aligned) {
+    MatmulChoice c{};
+    c.kernel = kMatmulTile64;
+    c.aligned = is_aligned;
+    const int cols = L->w_up ? 32 : 64;
+    const int64_t tm = grouped ? ragged_tiles(rows, L->n_groups, 64) : tiles(rows, 64);
+    const int64_t tn = tiles(L->out_features, cols);
+    c.tiles_m = (int)tm;
+    c.tiles_n = tm * tn > kMaxBlocks ? 0 : (int)tn;  // 0: too many workgroups
+    c.workspace = 0;
+    return c;
+}
+
+static bool linear_aligned(const moe_linear_t *L) {
+    const int64_t per = 16 / (int64_t)dtype_size(L->dtype);
+    if (L->in_features % per || !aligned(L->w, 16) || (L->w_up && !aligned(L->w_up, 16))) return false;
+    if (stride_or(L->row_stride, L->in_features) % per) return false;
+    return L->n_groups == 1 || L->group_stride % per == 0;
+}
+
+moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride, int32_t rows, int32_t top_k,
+                          int32_t rows_mode, const moe_plan_t *plan, const void *residual, int32_t residual_dtype,
+                          int64_t residual_stride, void *out, int64_t out_stride, void *workspace,
+                          size_t workspace_bytes, MatmulArgs *a, MatmulChoice *choice) {
+    const moe_status st = check_linear(L);
+    if (st != MOE_OK) return st;
+    const bool grouped = rows_mode != kRowsDense;
+    a->rows = 0;
+    if (rows < 0 || x_stride < 0 || out_stride < 0 || residual_stride < 0) return MOE_ERR_INVALID_ARG;
+    if (!grouped && L->n_groups != 1) return MOE_ERR_INVALID_ARG;
+    if (grouped && (rows_mode < MOE_ROWS_TOKEN || rows_mode > MOE_ROWS_SORTED || top_k < 1))
+        return MOE_ERR_INVALID_ARG;
+    if (residual && !dtype_ok(residual_dtype)) return MOE_ERR_INVALID_ARG;
+    if (rows > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    if (grouped && (!plan || !plan->work || !aligned(plan->work, 16) ||
+                    (rows_mode != MOE_ROWS_SORTED && !plan->sorted_slots)))
+        return MOE_ERR_INVALID_ARG;
+    const size_t es = dtype_size(L->dtype), os = dtype_size(L->out_dtype);
+    const size_t rs = residual ? dtype_size(residual_dtype) : 1;
+    if (!x || !out || !aligned(x, es) || !aligned(out, os) || (residual && !aligned(residual, rs)))
+        return MOE_ERR_INVALID_ARG;
+    const int64_t xs = stride_or(x_stride, L->in_features), os_row = stride_or(out_stride, L->out_features);
+    const int64_t rs_row = stride_or(residual_stride, L->out_features);
+    if (xs < L->in_features || os_row < L->out_features || (residual && rs_row < L->out_features))
+        return MOE_ERR_INVALID_ARG;
+    if (xs >= kMaxRowBytes / (int64_t)es || os_row >= kMaxRowBytes / (int64_t)os ||
+        (residual && rs_row >= kMaxRowBytes / (int64_t)rs))
+        return MOE_ERR_UNSUPPORTED;
+
+    const bool al = linear_aligned(L) && aligned(x, 16) && xs * (int64_t)es % 16 == 0;
+    *choice = choose_matmul(L, rows, grouped, al);
+    if (choice->tiles_n == 0) return MOE_ERR_UNSUPPORTED;
+
+    // out overlaps nothing that the call reads, itself as the residual apart
+    const int64_t row = stride_or(L->row_stride, L->in_features);
+    const int64_t group = stride_or(L->group_stride, (int64_t)L->out_features * row);
+    const int64_t bias_group = stride_or(L->bias_stride, L->out_features);
+    const int64_t x_rows = grouped && rows_mode == MOE_ROWS_TOKEN ? tiles(rows, top_k) : rows;
+    const Span so{out, rows, L->out_features * (int64_t)os, os_row * (int64_t)os};
+    const int64_t mat = (L->out_features - 1) * row + L->in_features;
+    const Span reads[5] = {{x, x_rows, L->in_features * (int64_t)es, xs * (int64_t)es},
+                           {L->w, L->n_groups, mat * (int64_t)es, group * (int64_t)es},
+                           {L->w_up, L->w_up ? L->n_groups : 0, mat * (int64_t)es, group * (int64_t)es},
+                           {L->bias, L->bias ? L->n_groups : 0, L->out_features * (int64_t)es, bias_group * (int64_t)es},
+                           {L->bias_up, L->bias_up ? L->n_groups : 0, L->out_features * (int64_t)es,
+                            bias_group * (int64_t)es}};
+    for (const Span &s : reads)
+        if (spans_overlap(so, s)) return MOE_ERR_INVALID_ARG;
+    const Span sr{residual, residual ? rows : 0, L->out_features * (int64_t)rs, rs_row * (int64_t)rs};
+    if (spans_overlap(so, sr) && !(residual == out && residual_dtype == L->out_dtype && rs_row == os_row))
+        return MOE_ERR_INVALID_ARG;
+    if (choice->workspace) {
+        if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+        if (workspace_bytes < choice->workspace) return MOE_ERR_WORKSPACE;
+        const Span sw{workspace, 1, (int64_t)choice->workspace, (int64_t)choice->workspace};
+        if (spans_overlap(sw, so) || spans_overlap(sw, sr)) return MOE_ERR_INVALID_ARG;
+        for (const Span &s : reads)
+            if (spans_overlap(sw, s)) return MOE_ERR_INVALID_ARG;
+    }
+
+    *a = MatmulArgs{};
+    a->x = (const char *)x;
+    a->w = (const char *)L->w;
+    a->w_up = (const char *)L->w_up;
+    a->bias = (const char *)L->bias;
+    a->bias_up = (const char *)L->bias_up;
+    a->residual = residual;
+    a->out = out;
+    a->x_stride = xs * (int64_t)es;
+    a->w_row = row * (int64_t)es;
+    a->w_group = group * (int64_t)es;
+    a->bias_group = bias_group * (int64_t)es;
+    a->res_stride = rs_row;
+    a->out_stride = os_row;
+    a->work = grouped ? (const int4 *)plan->work : nullptr;
+    a->slots = grouped && rows_mode != MOE_ROWS_SORTED ? plan->sorted_slots : nullptr;
+    a->rows = rows;
+    a->K = L->in_features;
+    a->N = L->out_features;
+    a->groups = L->n_groups;
+    a->top_k = grouped ? top_k : 1;
+    a->rows_mode = rows_mode;
+    a->fn = L->fn;
+    a->clamp = L->clamp_limit;
+    a->res_dtype = residual ? residual_dtype : L->out_dtype;
+    a->out_dtype = L->out_dtype;
+    a->vec_out = aligned(out, 4 * os) && os_row % 4 == 0 &&
+                 (!residual || (aligned(residual, 4 * rs) && rs_row % 4 == 0));
+    a->n_records = rows < L->n_groups ? rows : L->n_groups;
+    a->tiles_m = choice->tiles_m;
+    a->tiles_n = choice->tiles_n;
+    return MOE_OK;
+}
+
+moe_status check_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx, const float *topk_w,
+                         int32_t n_tokens, int32_t hidden, int32_t top_k, int32_t n_experts, const void *residual,
+                         int32_t residual_dtype, const void *out, int32_t out_dtype) {
+    if (n_tokens < 0 || hidden < 1 || top_k < 1 || n_experts < 1) return MOE_ERR_INVALID_ARG;
+    if (!dtype_ok(y_dtype) || !dtype_ok(out_dtype) || (residual && !dtype_ok(residual_dtype)))
+        return MOE_ERR_INVALID_ARG;
+    if (top_k > MOE_MAX_TOP_K || n_experts > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
+    const int64_t groups = tiles(hidden, 4);
+    if (hidden >= kMaxRowBytes / 4 || tiles(groups * n_tokens, 256) > kMaxBlocks ||
+        (int64_t)n_tokens * top_k > INT32_MAX / 2)
+        return MOE_ERR_UNSUPPORTED;
+    if (n_tokens == 0) return MOE_OK;
+    const size_t ys = dtype_size(y_dtype), os = dtype_size(out_dtype);
+    const size_t rs = residual ? dtype_size(residual_dtype) : 1;
+    if (!y || !topk_idx || !topk_w || !out) return MOE_ERR_INVALID_ARG;
+    if (!aligned(y, ys) || !aligned(out, os) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) ||
+        (residual && !aligned(residual, rs)))
+        return MOE_ERR_INVALID_ARG;
+    const int64_t slots = (int64_t)n_tokens * top_k, elems = (int64_t)n_tokens * hidden;
+    const Span so{out, 1, elems * (int64_t)os, elems * (int64_t)os};
+    const Span reads[3] = {{y, 1, slots * hidden * (int64_t)ys, 1}, {topk_idx, 1, slots * 4, 1}, {topk_w, 1, slots * 4, 1}};
+    for (const Span &s : reads)
+        if (spans_overlap(so, s)) return MOE_ERR_INVALID_ARG;
+    const Span sr{residual, residual ? 1 : 0, elems * (int64_t)rs, 1};
+    if (spans_overlap(so, sr) && !(residual == out && residual_dtype == out_dtype)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+}  // namespace moe
+
+extern "C" {
+
+moe_status moe_linear_check(const moe_linear_t *linear) { return moe::check_linear(linear); }
+
+// The size does not depend on x, so it covers the choice of either alignment.
+static size_t matmul_workspace(const moe_linear_t *linear, int32_t max_rows, bool grouped) {
+    if (moe::check_linear(linear) != MOE_OK || max_rows < 1) return 0;
+    const size_t a = moe::choose_matmul(linear, max_rows, grouped, true).workspace;
+    const size_t b = moe::choose_matmul(linear, max_rows, grouped, false).workspace;
+    return a > b ? a : b;
+}
+
+size_t moe_matmul_workspace_size(const moe_linear_t *linear, int32_t max_rows) {
+    return matmul_workspace(linear, max_rows, false);
+}
+
+size_t moe_grouped_workspace_size(const moe_linear_t *linear, int32_t max_slots) {
+    return matmul_workspace(linear, max_slots, true);
+}
+
+}  // extern "C"
