@@ -539,8 +539,9 @@ def decode_layer_static(layer: DeviceLayer, x: torch.Tensor, logits: torch.Tenso
 # --------------------------------------------------- unquantised products
 # These run on the current stream of the tensors' own device (or on `stream`),
 # whichever device is current, and what they allocate belongs to that stream.
-# They sit on the path of every decoded token, so a call that needs no
-# switch of device or stream makes none.
+# They sit on the path of every decoded token, where the host's time per call
+# is longer than a small product's on the device: the checks of a call that fits are
+# one pass of comparisons, and a message is put together only for one that does not.
 @dataclass
 class Linear:
     """Weights of a product plus the ABI descriptor (moe_linear_t) pointing at them."""
@@ -554,6 +555,10 @@ class Linear:
     n_groups: int
     out_dtype: torch.dtype
     struct: LinearStruct
+
+    def __post_init__(self):
+        self.dtype, self.device = self.w.dtype, self.w.device
+        self._ref = C.byref(self.struct)
 
     @staticmethod
     def from_tensors(w: torch.Tensor, bias: Optional[torch.Tensor] = None, w_up: Optional[torch.Tensor] = None,
@@ -628,25 +633,26 @@ def alloc_grouped_workspace(linear: Linear, max_slots: int) -> Optional[torch.Te
     return _alloc_bytes(grouped_workspace_size(linear, max_slots), linear.w.device)
 
 
+_get_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _on(device: torch.device, stream, call):
     """call(stream handle) with `device` current and `stream` (default: that device's
     current one) the stream that allocations belong to."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return call(torch._C._cuda_getCurrentRawStream(device.index))
         with torch.cuda.device(device):
-            return call(torch._C._cuda_getCurrentRawStream(device.index))
+            return call(_raw_stream(device.index))
     if stream.device != device:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
     with torch.cuda.stream(stream):
         return call(stream.cuda_stream)
 
 
-def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between the rows of a 2-D tensor with contiguous rows, 0 when it has one row."""
-    rows, cols = t.shape
+def _strides(t: torch.Tensor, rows: int, cols: int, name: str) -> int:
+    """Elements between the rows of a [rows, cols] tensor with contiguous rows, 0 when it has one row."""
     s0, s1 = t.stride()
-    if cols > 1 and s1 != 1:
+    if s1 != 1 and cols > 1:
         raise ValueError(f"the rows of {name} must be contiguous")
     if rows <= 1:
         return 0
@@ -655,32 +661,18 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     return s0
 
 
-def _out_2d(out: Optional[torch.Tensor], rows: int, cols: int, dtype, device) -> torch.Tensor:
-    if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device)
-    if out.dtype != dtype or out.shape != (rows, cols) or out.device != device:
-        raise ValueError(f"out must be a {dtype} [{rows}, {cols}] tensor on {device}, "
-                         f"got {out.dtype} {tuple(out.shape)} on {out.device}")
-    return out
+def _refuse(name: str, t: torch.Tensor, rows, cols: int, dtype, device):
+    raise ValueError(f"{name} must be a {dtype} [{rows}, {cols}] tensor on {device}, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _workspace(workspace: Optional[torch.Tensor], need: int, device):
-    """(pointer, bytes) of the caller's workspace, or of one allocated here for the call;
-    the tensor comes back too, to live until the call is enqueued."""
+def _workspace(workspace: Optional[torch.Tensor], need, linear: Linear, rows: int):
+    """The caller's workspace, or one allocated for the call where it needs one."""
     if workspace is None:
-        if need == 0:
-            return None, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    elif workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _check_product_x(linear: Linear, x: torch.Tensor):
-    w = linear.w
-    if x.dim() != 2 or x.dtype != w.dtype or x.device != w.device or x.shape[1] != linear.in_features:
-        raise ValueError(f"x must be a {w.dtype} [rows, {linear.in_features}] tensor on {w.device}, "
-                         f"got {x.dtype} {tuple(x.shape)} on {x.device}")
+        return _alloc_bytes(need(linear._ref, rows), linear.device)
+    if workspace.device != linear.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {linear.device}")
+    return workspace
 
 
 def matmul(linear: Linear, x: torch.Tensor, residual: Optional[torch.Tensor] = None,
@@ -688,25 +680,36 @@ def matmul(linear: Linear, x: torch.Tensor, residual: Optional[torch.Tensor] = N
     """moe_matmul: x [rows, in] -> out [rows, out] = residual + f(x w^T + bias), f gated when the
     linear has w_up.  Rows of x, residual and out may be strided; residual is any of the three
     types; out may be residual itself."""
-    _check_product_x(linear, x)
-    device, rows = x.device, x.shape[0]
-    xs = _row_stride(x, "x")
-    res = res_type = res_stride = 0
+    device = linear.device
+    if stream is not None or _get_device() != device.index:
+        return _on(device, stream, lambda handle: _matmul(linear, x, residual, out, workspace, handle))
+    return _matmul(linear, x, residual, out, workspace, _raw_stream(device.index))
+
+
+def _matmul(linear, x, residual, out, workspace, handle):
+    device, K, N = linear.device, linear.in_features, linear.out_features
+    if x.dim() != 2 or x.shape[1] != K or x.dtype is not linear.dtype or x.device != device:
+        _refuse("x", x, "rows", K, linear.dtype, device)
+    rows = x.shape[0]
+    res = None
+    res_type = res_stride = 0
     if residual is not None:
-        if residual.shape != (rows, linear.out_features) or residual.device != device or residual.dtype not in _DTYPES:
-            raise ValueError(f"residual must be a [{rows}, {linear.out_features}] bf16, fp16 or fp32 tensor on {device}")
-        res, res_type = residual.data_ptr(), _DTYPES[residual.dtype]
-        res_stride = _row_stride(residual, "residual")
-
-    def call(handle):
-        o = _out_2d(out, rows, linear.out_features, linear.out_dtype, device)
-        need = 0 if workspace is not None else matmul_workspace_size(linear, rows)
-        wp, wb, keep = _workspace(workspace, need, device)
-        _check(lib().moe_matmul(C.byref(linear.struct), x.data_ptr(), xs, rows, res or None, res_type, res_stride,
-                                o.data_ptr(), _row_stride(o, "out"), wp, wb, handle), "moe_matmul")
-        return o
-
-    return _on(device, stream, call)
+        res_type = _DTYPES.get(residual.dtype)
+        if residual.shape != (rows, N) or residual.device != device or res_type is None:
+            _refuse("residual", residual, rows, N, "bf16, fp16 or fp32", device)
+        res, res_stride = residual.data_ptr(), _strides(residual, rows, N, "residual")
+    if out is None:
+        out = torch.empty((rows, N), dtype=linear.out_dtype, device=device)
+    elif out.shape != (rows, N) or out.dtype is not linear.out_dtype or out.device != device:
+        _refuse("out", out, rows, N, linear.out_dtype, device)
+    L = lib()
+    ws = _workspace(workspace, L.moe_matmul_workspace_size, linear, rows)
+    st = L.moe_matmul(linear._ref, x.data_ptr(), _strides(x, rows, K, "x"), rows, res, res_type, res_stride,
+                      out.data_ptr(), _strides(out, rows, N, "out"), None if ws is None else ws.data_ptr(),
+                      0 if ws is None else ws.numel() * ws.element_size(), handle)
+    if st:
+        raise MoeError(st, "moe_matmul")
+    return out
 
 
 def grouped_matmul(linear: Linear, x: torch.Tensor, plan: Plan, n_slots: int, top_k: int = 1, rows: str = "token",
@@ -716,31 +719,43 @@ def grouped_matmul(linear: Linear, x: torch.Tensor, plan: Plan, n_slots: int, to
     row per token, slot s reads row s // top_k), "slot" (x has a row per slot) or "sorted"
     (rows of x and out lie grouped by expert, in the plan's order).  Rows of slots that the
     plan does not list are left as they are (unset when out is allocated here)."""
-    if rows not in _ROWS:
+    device = linear.device
+    if stream is not None or _get_device() != device.index:
+        return _on(device, stream,
+                   lambda handle: _grouped(linear, x, plan, n_slots, top_k, rows, out, workspace, handle))
+    return _grouped(linear, x, plan, n_slots, top_k, rows, out, workspace, _raw_stream(device.index))
+
+
+def _grouped(linear, x, plan, n_slots, top_k, rows, out, workspace, handle):
+    device, K, N = linear.device, linear.in_features, linear.out_features
+    mode = _ROWS.get(rows)
+    if mode is None:
         raise ValueError(f"rows must be one of {sorted(_ROWS)}")
-    _check_product_x(linear, x)
-    device, mode, n_slots, top_k = x.device, _ROWS[rows], int(n_slots), int(top_k)
     if n_slots < 0 or top_k < 1:
         raise ValueError("n_slots must be at least 0 and top_k at least 1")
-    if x.shape[0] != (-(-n_slots // top_k) if mode == MOE_ROWS_TOKEN else n_slots):
-        raise ValueError(f"x has {x.shape[0]} rows, which does not fit {n_slots} slots with rows={rows!r}, top_k={top_k}")
+    if x.dim() != 2 or x.shape[1] != K or x.dtype is not linear.dtype or x.device != device:
+        _refuse("x", x, "rows", K, linear.dtype, device)
+    x_rows = x.shape[0]
+    if x_rows != (-(-n_slots // top_k) if mode == MOE_ROWS_TOKEN else n_slots):
+        raise ValueError(f"x has {x_rows} rows, which does not fit {n_slots} slots with rows={rows!r}, top_k={top_k}")
     work, slots = plan.work, plan.sorted_slots
     if work.numel() < 4 * min(linear.n_groups, max(n_slots, 1)) or work.device != device:
         raise ValueError(f"the plan's records are too few for {linear.n_groups} experts or not on {device}")
     if mode != MOE_ROWS_SORTED and (slots.numel() < n_slots or slots.device != device):
         raise ValueError(f"the plan's sorted_slots are fewer than {n_slots} or not on {device}")
-    xs = _row_stride(x, "x")
-
-    def call(handle):
-        o = _out_2d(out, n_slots, linear.out_features, linear.out_dtype, device)
-        need = 0 if workspace is not None else grouped_workspace_size(linear, n_slots)
-        wp, wb, keep = _workspace(workspace, need, device)
-        _check(lib().moe_grouped_matmul(C.byref(linear.struct), x.data_ptr(), xs, n_slots, top_k, mode,
-                                        C.byref(plan.struct), o.data_ptr(), _row_stride(o, "out"), wp, wb, handle),
-               "moe_grouped_matmul")
-        return o
-
-    return _on(device, stream, call)
+    if out is None:
+        out = torch.empty((n_slots, N), dtype=linear.out_dtype, device=device)
+    elif out.shape != (n_slots, N) or out.dtype is not linear.out_dtype or out.device != device:
+        _refuse("out", out, n_slots, N, linear.out_dtype, device)
+    L = lib()
+    ws = _workspace(workspace, L.moe_grouped_workspace_size, linear, n_slots)
+    st = L.moe_grouped_matmul(linear._ref, x.data_ptr(), _strides(x, x_rows, K, "x"), n_slots, top_k, mode,
+                              C.byref(plan.struct), out.data_ptr(), _strides(out, n_slots, N, "out"),
+                              None if ws is None else ws.data_ptr(),
+                              0 if ws is None else ws.numel() * ws.element_size(), handle)
+    if st:
+        raise MoeError(st, "moe_grouped_matmul")
+    return out
 
 
 def combine(y: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, n_experts: int,
@@ -749,38 +764,42 @@ def combine(y: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, n_experts: int,
     """moe_combine: y [B * k, H], idx int32 [B, k], w fp32 [B, k] -> out [B, H] =
     residual + the weighted sum of each token's k rows.  out_dtype defaults to out's type, else
     the residual's, else y's."""
-    if y.dim() != 2 or y.dtype not in _DTYPES or not y.is_contiguous() or not y.is_cuda:
+    device = y.device
+    if not y.is_cuda:
         raise ValueError("y must be a contiguous bf16, fp16 or fp32 [slots, hidden] device tensor")
-    device, H = y.device, y.shape[1]
-    if idx.dim() != 2 or idx.dtype != torch.int32 or not idx.is_contiguous() or idx.device != device:
+    if stream is not None or _get_device() != device.index:
+        return _on(device, stream, lambda handle: _combine(y, idx, w, n_experts, residual, out, out_dtype, handle))
+    return _combine(y, idx, w, n_experts, residual, out, out_dtype, _raw_stream(device.index))
+
+
+def _combine(y, idx, w, n_experts, residual, out, out_dtype, handle):
+    device, y_type = y.device, _DTYPES.get(y.dtype)
+    if y.dim() != 2 or y_type is None or not y.is_contiguous():
+        raise ValueError("y must be a contiguous bf16, fp16 or fp32 [slots, hidden] device tensor")
+    H = y.shape[1]
+    if idx.dim() != 2 or idx.dtype is not torch.int32 or not idx.is_contiguous() or idx.device != device:
         raise ValueError(f"idx must be a contiguous int32 [B, k] tensor on {device}")
     B, k = idx.shape
-    if w.dtype != torch.float32 or w.shape != idx.shape or not w.is_contiguous() or w.device != device:
-        raise ValueError(f"w must be a contiguous fp32 [{B}, {k}] tensor on {device}")
+    if w.dtype is not torch.float32 or w.shape != idx.shape or not w.is_contiguous() or w.device != device:
+        _refuse("w", w, B, k, "contiguous fp32", device)
     if y.shape[0] != B * k:
         raise ValueError(f"y has {y.shape[0]} rows, {B * k} needed for {B} tokens of {k} slots")
-    res = res_type = 0
+    res, res_type = None, 0
     if residual is not None:
-        if (residual.shape != (B, H) or residual.device != device or residual.dtype not in _DTYPES
-                or not residual.is_contiguous()):
-            raise ValueError(f"residual must be a contiguous [{B}, {H}] bf16, fp16 or fp32 tensor on {device}")
-        res, res_type = residual.data_ptr(), _DTYPES[residual.dtype]
-    if out is not None:
-        if out_dtype is not None and out.dtype != out_dtype:
-            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
-        out_dtype = out.dtype
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous")
-    elif out_dtype is None:
-        out_dtype = y.dtype if residual is None else residual.dtype
-    if out_dtype not in _DTYPES:
-        raise ValueError("out must be bf16, fp16 or fp32")
-
-    def call(handle):
-        o = _out_2d(out, B, H, out_dtype, device)
-        _check(lib().moe_combine(y.data_ptr(), _DTYPES[y.dtype], idx.data_ptr(), w.data_ptr(), B, H, k,
-                                 int(n_experts), res or None, res_type, o.data_ptr(), _DTYPES[out_dtype], handle),
-               "moe_combine")
-        return o
-
-    return _on(device, stream, call)
+        res_type = _DTYPES.get(residual.dtype)
+        if residual.shape != (B, H) or residual.device != device or res_type is None or not residual.is_contiguous():
+            _refuse("residual", residual, B, H, "contiguous bf16, fp16 or fp32", device)
+        res = residual.data_ptr()
+    if out is None:
+        if out_dtype is None:
+            out_dtype = y.dtype if residual is None else residual.dtype
+        out = torch.empty((B, H), dtype=out_dtype, device=device)
+    out_type = _DTYPES.get(out.dtype)
+    if (out.shape != (B, H) or out.device != device or out_type is None or not out.is_contiguous()
+            or (out_dtype is not None and out.dtype is not out_dtype)):
+        _refuse("out", out, B, H, f"contiguous {out_dtype or 'bf16, fp16 or fp32'}", device)
+    st = lib().moe_combine(y.data_ptr(), y_type, idx.data_ptr(), w.data_ptr(), B, H, k, n_experts, res, res_type,
+                           out.data_ptr(), out_type, handle)
+    if st:
+        raise MoeError(st, "moe_combine")
+    return out

@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB_NAME = "libmoe_decode.so"
 LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 SOURCES = ["abi.cpp", "route.hip", "expert.hip", "gate_up_route.hip", "generic.hip", "pack.hip", "router_proj.hip", "tile.hip",
-           "matmul_abi.cpp", "matmul.hip", "combine.hip"]
+           "matmul_abi.cpp", "matmul.hip", "matmul_tile.hip", "matmul_deep.hip", "matmul_few.hip",
+           "combine.hip"]
 ARCH = "gfx950"
 
 

@@ -99,25 +99,9 @@ __global__ __launch_bounds__(256) void matmul_tile64_kernel(MatmulArgs a) {
     }
 
     const int col = col0 + wn * CW + g * 4 * NTC;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        mm_f32x4 *z = acc[m];
-        if (a.bias) {
-            add_bias<DT, NTC>(z, a.bias + (int64_t)t.group * a.bias_group, col, a.N);
-            if constexpr (GATED) add_bias<DT, NTC>(z + NTC, a.bias_up + (int64_t)t.group * a.bias_group, col, a.N);
-        }
-        clip_all<NT>(z, a.clamp);
-        apply_fn<NTC>(z, a.fn);
-        if constexpr (GATED)
-#pragma unroll
-            for (int n = 0; n < NTC; ++n) z[n] *= z[n + NTC];
-        const int o = orow[wm * 32 + m * 16 + r16];
-        if (o < 0) continue;
-#pragma unroll
-        for (int n = 0; n < NTC; ++n)
-            store4(a.out, (int64_t)o * a.out_stride, a.out_dtype, a.residual, (int64_t)o * a.res_stride, a.res_dtype,
-                   a.vec_out, col + 4 * n, a.N, z[n]);
-    }
+    mm_f32x4 b[NT];
+    load_bias<DT, GATED, NT>(a, t.group, col, b);
+    static_for<MT>([&](auto m) { finish_row<GATED, NT>(a, orow[wm * 32 + m * 16 + r16], col, acc[m], b); });
 }
 
 template <int DT, bool GATED, bool ALIGNED>
@@ -137,6 +121,13 @@ static void launch_dtype(const MatmulArgs &a, const MatmulChoice &c, hipStream_t
 moe_status launch_matmul(const moe_linear_t *linear, const MatmulArgs &a, const MatmulChoice &c, void *workspace,
                          hipStream_t s) {
     (void)workspace;
+    if (c.kernel == kMatmulTile)
+        launch_matmul_tile(linear->dtype, a, c, s);
+    else if (c.kernel == kMatmulDeep)
+        launch_matmul_deep(linear->dtype, a, c, s);
+    else if (c.kernel == kMatmulFew)
+        launch_matmul_few(linear->dtype, a, c, s);
+    else
     switch (linear->dtype) {
         case MOE_DTYPE_BF16: launch_dtype<MOE_DTYPE_BF16>(a, c, s); break;
         case MOE_DTYPE_F16: launch_dtype<MOE_DTYPE_F16>(a, c, s); break;

@@ -70,17 +70,62 @@ static int64_t ragged_tiles(int64_t rows, int64_t groups, int64_t tile) {
     return (rows + used * (tile - 1)) / tile;
 }
 
+// Microseconds that a kernel takes, roughly: `fixed` for a launch, then for every
+// 256 tiles (a tile on each CU) `round` and `step` for each 128 bytes of a row, at
+// least `alone` a step when the tiles are fewer.  Fitted to measurements of
+// every kernel on one another's shapes (dense: 1 to 4096 rows, K 768 to 8192, N 512 to 4096; grouped: 1 to
+// 4096 tokens, 128 experts, top-8, K 768 and 2048), where the choice made with it
+// is within 10 % of the best kernel.  What separates them: below some 64 rows
+// splitting K over a workgroup's waves wins (2048 x 2048 bf16, 16 rows: 6.2 us
+// against 8.8 of the 64 x 64 tile), then the tile grows with the work (1024 rows:
+// 64 x 128 13.8, 64 x 64 16.1, 128 x 128 24.1 us; 4096 rows: 128 x 128 37.1, 64 x
+// 128 43.1, 256 x 256 60.4 us; 8192 rows of K 8192, N 4096: 256 x 256 432 us, 128 x
+// 128 507 us).  fp32 steps take some three times as long: the matrix cores'
+// rate.
+struct Cost {
+    MatmulKernel kernel;
+    int mt, nt;
+    double fixed, round, step, alone;
+};
+static const Cost kCosts[] = {
+    {kMatmulDeep, 2, 2, 3.3, 0.3, 0.20, 0.19}, {kMatmulDeep, 2, 4, 3.3, 0.5, 0.37, 0.27},
+    {kMatmulTile, 4, 4, 3.3, 1.2, 0.53, 0.72}, {kMatmulTile, 8, 8, 3.3, 3.0, 1.70, 1.70},
+    {kMatmulAny, 2, 2, 3.3, 0.5, 0.30, 0.90},  {kMatmulFew, 1, 0, 2.7, 0.0, 0.116, 0.116},
+    {kMatmulFew, 2, 0, 2.7, 0.0, 0.170, 0.170}};
+
 MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bool is_aligned) {
-    MatmulChoice c{};
-    c.kernel = kMatmulTile64;
-    c.aligned = is_aligned;
-    const int cols = L->w_up ? 32 : 64;
-    const int64_t tm = grouped ? ragged_tiles(rows, L->n_groups, 64) : tiles(rows, 64);
-    const int64_t tn = tiles(L->out_features, cols);
-    c.tiles_m = (int)tm;
-    c.tiles_n = tm * tn > kMaxBlocks ? 0 : (int)tn;  // 0: too many workgroups
-    c.workspace = 0;
-    return c;
+    MatmulChoice best{};
+    best.aligned = is_aligned;
+    const bool f32 = L->dtype == MOE_DTYPE_F32, gated = L->w_up != nullptr;
+    const double steps = (double)tiles(L->in_features * (int64_t)dtype_size(L->dtype), 128);
+    const int64_t used = rows < L->n_groups ? rows : L->n_groups;
+    double best_time = 0;
+    for (const Cost &k : kCosts) {
+        const bool few = k.kernel == kMatmulFew;
+        if (few ? grouped : (k.kernel == kMatmulAny) == is_aligned) continue;  // no kernel for this call
+        if (f32 && k.mt == 8) continue;
+        const int64_t tile_rows = few ? 16 * k.mt : 32 * k.mt;
+        const int64_t tile_cols = few ? (gated && k.mt == 1 ? 8 : 16) : (gated ? 16 : 32) * k.nt;
+        const int64_t tm = grouped ? ragged_tiles(rows, L->n_groups, tile_rows) : tiles(rows, tile_rows);
+        const int64_t tn = tiles(L->out_features, tile_cols);
+        if (tm * tn > kMaxBlocks) continue;
+        // a group's last tile is half full on average
+        const double n = grouped ? ((double)rows / tile_rows + 0.5 * used) * tn : (double)(tm * tn);
+        const double rounds = n <= 256 ? 1 : (double)(int64_t)((n + 255) / 256);
+        double step = n <= 256 && k.alone > k.step ? k.alone : n <= 128 ? k.alone : k.step * rounds;
+        if (f32 && !few) step *= 3;
+        if (few && gated && k.mt == 2) step *= 1.4;
+        const double time = k.fixed + k.round * rounds + step * steps;
+        if (best.tiles_n == 0 || time < best_time) {
+            best_time = time;
+            best.kernel = k.kernel;
+            best.mt = k.mt;
+            best.nt = k.nt;
+            best.tiles_m = (int)tm;
+            best.tiles_n = (int)tn;
+        }
+    }
+    return best;  // tiles_n == 0: more workgroups than a launch takes
 }
 
 static bool linear_aligned(const moe_linear_t *L) {
@@ -120,7 +165,10 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
         (residual && rs_row >= kMaxRowBytes / (int64_t)rs))
         return MOE_ERR_UNSUPPORTED;
 
-    const bool al = linear_aligned(L) && aligned(x, 16) && xs * (int64_t)es % 16 == 0;
+    // gathered rows of x are 32-bit offsets from x in the kernels for aligned rows
+    const int64_t x_rows = grouped && rows_mode == MOE_ROWS_TOKEN ? tiles(rows, top_k) : rows;
+    const bool near = !grouped || rows_mode == MOE_ROWS_SORTED || x_rows * xs * (int64_t)es < (int64_t)UINT32_MAX;
+    const bool al = near && linear_aligned(L) && aligned(x, 16) && xs * (int64_t)es % 16 == 0;
     *choice = choose_matmul(L, rows, grouped, al);
     if (choice->tiles_n == 0) return MOE_ERR_UNSUPPORTED;
 
@@ -128,7 +176,6 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
     const int64_t row = stride_or(L->row_stride, L->in_features);
     const int64_t group = stride_or(L->group_stride, (int64_t)L->out_features * row);
     const int64_t bias_group = stride_or(L->bias_stride, L->out_features);
-    const int64_t x_rows = grouped && rows_mode == MOE_ROWS_TOKEN ? tiles(rows, top_k) : rows;
     const Span so{out, rows, L->out_features * (int64_t)os, os_row * (int64_t)os};
     const int64_t mat = (L->out_features - 1) * row + L->in_features;
     const Span reads[5] = {{x, x_rows, L->in_features * (int64_t)es, xs * (int64_t)es},
@@ -179,6 +226,7 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
     a->out_dtype = L->out_dtype;
     a->vec_out = aligned(out, 4 * os) && os_row % 4 == 0 &&
                  (!residual || (aligned(residual, 4 * rs) && rs_row % 4 == 0));
+    if (a->vec_out && aligned(out, 8 * os) && os_row % 8 == 0) a->vec_out = 2;
     a->n_records = rows < L->n_groups ? rows : L->n_groups;
     a->tiles_m = choice->tiles_m;
     a->tiles_n = choice->tiles_n;

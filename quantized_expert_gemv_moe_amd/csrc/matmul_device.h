@@ -46,6 +46,16 @@ constexpr int kElemBytes = DT == MOE_DTYPE_F32 ? 4 : 2;
 template <int DT>
 constexpr int kChunk = 16 / kElemBytes<DT>;  // elements of a 16-byte chunk
 
+// A whole chunk.
+template <int DT, bool ALIGNED>
+__device__ __forceinline__ mm_u32x4 load_whole(const char *p) {
+    struct __attribute__((packed, aligned(kElemBytes<DT>))) Chunk {
+        mm_u32x4 v;
+    };
+    if constexpr (ALIGNED) return *(const mm_u32x4 *)p;
+    return ((const Chunk *)p)->v;
+}
+
 // Chunk c of a row of K elements, zeros past its end.  ALIGNED: rows are
 // whole chunks at 16-byte addresses.  Otherwise rows start at any element
 // and may end inside a chunk: a whole chunk is one 16-byte load of element
@@ -57,13 +67,10 @@ __device__ __forceinline__ mm_u32x4 load_chunk(const char *row, int c, int K) {
     mm_u32x4 v = {0u, 0u, 0u, 0u};
     const int left = K - c * E;
     if constexpr (ALIGNED) {
-        if (left > 0) v = *(const mm_u32x4 *)(row + (int64_t)c * 16);
+        if (left > 0) v = load_whole<DT, true>(row + (int64_t)c * 16);
     } else {
-        struct __attribute__((packed, aligned(kElemBytes<DT>))) Chunk {
-            mm_u32x4 v;
-        };
         if (left >= E) {
-            v = ((const Chunk *)(row + (int64_t)c * 16))->v;
+            v = load_whole<DT, false>(row + (int64_t)c * 16);
         } else if (left > 0) {
 #pragma unroll
             for (int i = 0; i < E; ++i) {
@@ -126,16 +133,44 @@ __device__ __forceinline__ void store4(void *out, int64_t out_at, int out_dtype,
         }
         return;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (col + i >= N) break;
-        float f = v[i];
+#pragma unroll 1
+    for (int i = 0; i < 4 && col + i < N; ++i) {
+        float f = i == 0 ? v[0] : i == 1 ? v[1] : i == 2 ? v[2] : v[3];
         if (residual) f += load_value(residual, res_at + col + i, res_dtype);
         if (out_dtype == MOE_DTYPE_F32)
             ((float *)out)[out_at + col + i] = f;
         else
             ((uint16_t *)out)[out_at + col + i] = (uint16_t)round_pair(f, 0.f, out_dtype);
     }
+}
+
+// 4 NC consecutive columns of row o, in accumulators of four; 16-bit outputs go out
+// eight columns at a time where their addresses allow.
+template <int NC>
+__device__ __forceinline__ void store_row(const MatmulArgs &a, int o, int col, const mm_f32x4 *z) {
+    const int64_t out_at = (int64_t)o * a.out_stride, res_at = (int64_t)o * a.res_stride;
+    if constexpr (NC % 2 == 0) {
+        if (a.vec_out == 2 && a.out_dtype != MOE_DTYPE_F32 && col + 4 * NC <= a.N) {
+#pragma unroll
+            for (int n = 0; n < NC; n += 2) {
+                mm_f32x4 v0 = z[n], v1 = z[n + 1];
+                if (a.residual) {
+                    v0 += load_value4(a.residual, res_at + col + 4 * n, a.res_dtype);
+                    v1 += load_value4(a.residual, res_at + col + 4 * n + 4, a.res_dtype);
+                }
+                mm_u32x4 b;
+                b[0] = round_pair(v0[0], v0[1], a.out_dtype);
+                b[1] = round_pair(v0[2], v0[3], a.out_dtype);
+                b[2] = round_pair(v1[0], v1[1], a.out_dtype);
+                b[3] = round_pair(v1[2], v1[3], a.out_dtype);
+                *(mm_u32x4 *)((uint16_t *)a.out + out_at + col + 4 * n) = b;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+        store4(a.out, out_at, a.out_dtype, a.residual, res_at, a.res_dtype, a.vec_out != 0, col + 4 * n, a.N, z[n]);
 }
 
 // ------------------------------------------------------------ activations
@@ -168,17 +203,17 @@ __device__ __forceinline__ float clip(float z, float limit) {  // NaN stays NaN
 // z / (1 + exp(-z)); the reciprocal is good to 1 ulp.
 __device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
 
-// f over an array of accumulators.  The function is uniform over the launch,
-// so the choice is made once per array and not per element.
+// f over N accumulators.  The function is uniform over the launch, so the choice
+// is made once for all of them and not per element.
 template <int N>
 __device__ __forceinline__ void apply_fn(mm_f32x4 *z, int fn) {
-#define MOE_APPLY(EXPR)                                \
-    _Pragma("unroll") for (int i = 0; i < N; ++i) {    \
+#define MOE_APPLY(EXPR)                                 \
+    _Pragma("unroll") for (int n = 0; n < N; ++n) {     \
         _Pragma("unroll") for (int r = 0; r < 4; ++r) { \
-            const float v = z[i][r];                   \
-            z[i][r] = EXPR;                            \
-        }                                              \
-    }                                                  \
+            const float v = z[n][r];                    \
+            z[n][r] = EXPR;                             \
+        }                                               \
+    }                                                   \
     break
     switch (fn) {
         case MOE_FN_RELU: MOE_APPLY(v < 0.f ? 0.f : v);
@@ -191,28 +226,59 @@ __device__ __forceinline__ void apply_fn(mm_f32x4 *z, int fn) {
 #undef MOE_APPLY
 }
 
-// From accumulators to values before the residual: bias, clip, f, gate.
-// z holds N tiles of 4 columns for one row; `bias` points at the weights' type
-// for the columns col .. of tile i at col + 4 i (clamped to the last column,
-// whose value the store drops).
-template <int DT, int N>
-__device__ __forceinline__ void add_bias(mm_f32x4 *z, const char *bias, int col, int cols) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int c = col + 4 * i + r;
-            z[i][r] += load_value(bias, c < cols ? c : cols - 1, DT);
-        }
+// Calls f(0), f(1), ... with compile-time numbers.
+template <int I>
+struct Index {
+    static constexpr int value = I;
+    constexpr operator int() const { return I; }
+};
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void static_for(F &&f) {
+    if constexpr (I < N) {
+        f(Index<I>{});
+        static_for<N, I + 1>(f);
+    }
 }
 
-template <int N>
-__device__ __forceinline__ void clip_all(mm_f32x4 *z, float limit) {
-    if (limit > 0.f)
+// A row's accumulators to its stored values: bias, clip, f, gate, residual, one
+// rounding.  The lane holds columns col .. col + 4 NC - 1, gate in the first NC
+// accumulators and up in the others when gated.  b holds the columns' biases.
+template <bool GATED, int NT>
+__device__ __forceinline__ void finish_row(const MatmulArgs &a, int o, int col, mm_f32x4 *z, const mm_f32x4 *b) {
+    constexpr int NC = GATED ? NT / 2 : NT;
 #pragma unroll
-        for (int i = 0; i < N; ++i)
+    for (int n = 0; n < NT; ++n) z[n] += b[n];
+    if (a.clamp > 0.f) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) z[i][r] = clip(z[i][r], limit);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) z[n][r] = clip(z[n][r], a.clamp);
+    }
+    apply_fn<NC>(z, a.fn);
+    if constexpr (GATED) {
+#pragma unroll
+        for (int n = 0; n < NC; ++n) z[n] *= z[n + NC];
+    }
+    if (o >= 0) store_row<NC>(a, o, col, z);
+}
+
+// The biases of a lane's columns (zero without one; -0, which changes no sum).
+// Columns from N on take the last column's; the store drops them.
+template <int DT, bool GATED, int NT>
+__device__ __forceinline__ void load_bias(const MatmulArgs &a, int group, int col, mm_f32x4 *b) {
+    constexpr int NC = GATED ? NT / 2 : NT;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) b[n] = mm_f32x4{-0.f, -0.f, -0.f, -0.f};
+    if (!a.bias) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const char *p = (n < NC ? a.bias : a.bias_up) + (int64_t)group * a.bias_group;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int c = col + 4 * (n % NC) + r;
+            b[n][r] = load_value(p, c < a.N ? c : a.N - 1, DT);
+        }
+    }
 }
 
 // ------------------------------------------------------------ work division

@@ -28,17 +28,23 @@ struct MatmulArgs {
     int K, N, groups, top_k, rows_mode, fn;
     float clamp;
     int res_dtype, out_dtype;
-    int vec_out;         // out and residual take 4-column vector accesses
+    int vec_out;         // out and residual take vector accesses of 4 columns (1), out also of 8 (2)
     int n_records;       // plan records that can be in use
     int tiles_m, tiles_n;
 };
 
 // Kernels of a product.
-enum MatmulKernel { kMatmulTile64 = 0 };
+enum MatmulKernel {
+    kMatmulAny = 0,  // 64 x 64 tile through registers, any alignment
+    kMatmulTile,     // large tile straight into LDS, aligned rows
+    kMatmulDeep,     // small tile, many stages of LDS, aligned rows
+    kMatmulFew,      // few rows: w straight into registers, K split over waves
+};
 
 struct MatmulChoice {
     MatmulKernel kernel;
-    bool aligned;       // every row of x and w is whole, aligned 16-byte chunks
+    int mt, nt;    // tile: 32 mt rows of x by 32 nt rows of w; kMatmulFew: 16 mt rows of x
+    bool aligned;  // every row of x and w is whole, aligned 16-byte chunks
     int tiles_m, tiles_n;
     size_t workspace;
 };
@@ -65,6 +71,10 @@ moe_status check_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx
                          int32_t n_tokens, int32_t hidden, int32_t top_k, int32_t n_experts,
                          const void *residual, int32_t residual_dtype, const void *out, int32_t out_dtype);
 
+// The tile kernels that load straight into LDS (matmul_tile.hip).
+void launch_matmul_tile(int dtype, const MatmulArgs &args, const MatmulChoice &choice, hipStream_t stream);
+void launch_matmul_deep(int dtype, const MatmulArgs &args, const MatmulChoice &choice, hipStream_t stream);
+void launch_matmul_few(int dtype, const MatmulArgs &args, const MatmulChoice &choice, hipStream_t stream);
 moe_status launch_matmul(const moe_linear_t *linear, const MatmulArgs &args, const MatmulChoice &choice,
                          void *workspace, hipStream_t stream);
 

@@ -1,0 +1,279 @@
+// Large tiles of the unquantised products (gfx950): x and w go from global
+// memory straight into LDS.
+//
+// Four waves, 2 x 2, each (16 MT) x (16 NT) of the workgroup's (32 MT) x (32 NT)
+// tile (rows of x times rows of w).  A step covers 128 bytes of every row.
+// Each stage of LDS holds a step as four half tiles, X0 X1 (each wave's first
+// and second half of its rows of x) and W0 W1 (of its rows of w), and a step is
+// four phases, one quadrant of a wave's tile each:
+//   phase  multiplies  reads into registers  loads into LDS
+//   0      X0 W0       W1 of this step       W0 two steps on
+//   1      X0 W1       X1 of this step       W1 two steps on
+//   2      X1 W1       X0 of the next step   X1 two steps on
+//   3      X1 W0       W0 of the next step   X0 three steps on
+// A half tile is overwritten one phase after its last reader read it and needed
+// seven phases after its load was issued, so loads have seven phases to
+// arrive while the matrix cores work, with two stages of LDS.  Every phase
+// starts with a wait for the loads it reads (the later six half tiles may still
+// be on their way), for the wave's own LDS reads, and a barrier.
+//
+// The loads (global_load_lds_dwordx4) put lane l's 16 bytes at l * 16 of a
+// 1 KiB block, eight rows of 128 bytes; the swizzle that spreads the 16 rows
+// a quarter wave reads over the banks is therefore made on the global side: lane l
+// fetches chunk (l % 8) ^ ((row / 2) % 8) of its row.  They are issued as inline
+// assembly without results, because the compiler would wait for all loads in
+// flight before any LDS read that may alias their target; the waits that
+// replace it are written out.
+#include <hip/hip_runtime.h>
+
+#include "matmul_device.h"
+#include "matmul_internal.h"
+#include "matmul_lds.h"
+
+namespace moe {
+
+// One 64-byte step with the accumulator held in accumulation registers: a wave's 64
+// accumulators fill all 256 of them, and the compiler, left to choose, mixes
+// the two register files and moves operands between them.  The compiler knows nothing of
+// the waits that matrix instructions need, so what reads an accumulator next goes through
+// settle() first, and so does what is written before the first step.
+template <int DT>
+__device__ __forceinline__ void mma_acc(const mm_u32x4 &a, const mm_u32x4 &b, mm_f32x4 &c) {
+    if constexpr (DT == MOE_DTYPE_BF16)
+        asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else
+        asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+template <int MT, int NT>
+__device__ __forceinline__ void settle(mm_f32x4 (*c)[NT]) {
+    asm volatile("s_nop 15\n\ts_nop 15");
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) asm volatile("" : "+a"(c[m][n]));
+}
+
+template <int DT, bool GATED, int MT, int NT>
+__global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
+    constexpr int BM = 32 * MT;                      // rows of x; of w 32 NT
+    constexpr int NTC = GATED ? NT / 2 : NT;         // column tiles of a wave
+    constexpr int CW = NTC * 16;                     // columns of a wave
+    constexpr int XI = MT / 2, WI = NT / 2;          // loads a wave issues for a half tile
+    constexpr int XH = 16 * MT * 128, WH = 16 * NT * 128;  // bytes of a half tile
+    constexpr int STAGE = 2 * XH + 2 * WH;
+    constexpr bool ACC = MT * NT == 64;              // accumulators fill their registers
+    static_assert(!ACC || DT != MOE_DTYPE_F32, "the large tile is for 16-bit operands");
+    __shared__ __align__(1024) char lds[2 * STAGE];
+    __shared__ int orow[BM];
+    MatmulTile t;
+    if (a.rows_mode == kRowsDense ? !dense_tile<8>(a, BM, &t) : !grouped_tile(a, BM, &t)) return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int g = lane >> 4, r16 = lane & 15;
+    const int col0 = t.tile_n * 2 * CW;
+    for (int i = tid; i < BM; i += 256) orow[i] = out_row(a, t, t.row0 + i);
+    __syncthreads();
+
+    // Sources.  Rows of x as 32-bit offsets from a base: of the tile's first row
+    // where rows are in order, of x itself where they are gathered (the host
+    // sends an x of 4 GiB and more to the register kernel).
+    const bool gathered = a.rows_mode == MOE_ROWS_TOKEN || a.rows_mode == MOE_ROWS_SLOT;
+    const int first = t.first + t.row0;
+    const char *xbase = gathered ? a.x : a.x + (int64_t)first * a.x_stride;
+    const char *wbase = a.w + (int64_t)t.group * a.w_group + (int64_t)col0 * a.w_row;
+    const char *ubase = GATED ? a.w_up + (int64_t)t.group * a.w_group + (int64_t)col0 * a.w_row : wbase;
+    uint32_t xo[2][XI], wo[2][WI];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < XI; ++i) {
+            const int p = (wave * XI + i) * 8 + (lane >> 3);
+            const int c = (lane & 7) ^ ((p >> 1) & 7);
+            const int row = p / (8 * MT) * (16 * MT) + h * 8 * MT + p % (8 * MT);
+            const int o = orow[row];
+            const int xr = gathered ? x_row(a, o) : (t.row0 + row < t.count ? row : 0);
+            xo[h][i] = (uint32_t)xr * (uint32_t)a.x_stride + c * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < WI; ++i) {
+            const int p = (wave * WI + i) * 8 + (lane >> 3);
+            const int c = (lane & 7) ^ ((p >> 1) & 7);
+            const int q = p % (8 * NT), j = (GATED ? 0 : h * (NT / 2)) + (q >> 4), ar = q & 15;
+            int col = p / (8 * NT) * CW + (ar >> 2) * 4 * NTC + j * 4 + (ar & 3);
+            if (col0 + col >= a.N) col = a.N - 1 - col0;
+            wo[h][i] = (uint32_t)col * (uint32_t)a.w_row + c * 16;
+        }
+    }
+    const int chunks = (a.K * kElemBytes<DT>) >> 4;  // of a row
+    const int full = chunks >> 3, steps = (chunks + 7) >> 3;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+
+    auto load_x = [&](int h, int s, auto whole, auto part) {
+        const uint32_t at = lds0 + (s & 1) * STAGE + h * XH + wave * XI * 1024;
+        if (whole || s < full) {
+            const char *b = xbase + (int64_t)s * 128;
+#pragma unroll
+            for (int i = from(part, XI); i < upto(part, XI); ++i) dma16(at + i * 1024, b, xo[h][i]);
+        } else if (s < steps) {  // the last, partial step: zeros past the row's end
+#pragma unroll
+            for (int i = from(part, XI); i < upto(part, XI); ++i) {
+                const int p = (wave * XI + i) * 8 + (lane >> 3);
+                const int c = (lane & 7) ^ ((p >> 1) & 7);
+                dma16(at + i * 1024, s * 8 + c < chunks ? xbase + (int64_t)s * 128 + xo[h][i] : (const char *)&kZeroChunk);
+            }
+        }
+    };
+    auto load_w = [&](int h, int s, auto whole, auto part) {
+        const uint32_t at = lds0 + (s & 1) * STAGE + 2 * XH + h * WH + wave * WI * 1024;
+        const char *base = h ? ubase : wbase;
+        if (whole || s < full) {
+            const char *b = base + (int64_t)s * 128;
+#pragma unroll
+            for (int i = from(part, WI); i < upto(part, WI); ++i) dma16(at + i * 1024, b, wo[h][i]);
+        } else if (s < steps) {
+#pragma unroll
+            for (int i = from(part, WI); i < upto(part, WI); ++i) {
+                const int p = (wave * WI + i) * 8 + (lane >> 3);
+                const int c = (lane & 7) ^ ((p >> 1) & 7);
+                dma16(at + i * 1024, s * 8 + c < chunks ? base + (int64_t)s * 128 + wo[h][i] : (const char *)&kZeroChunk);
+            }
+        }
+    };
+
+    mm_f32x4 acc[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[m][n] = mm_f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (ACC) settle<MT, NT>(acc);
+    mm_u32x4 x0[MT / 2][2], x1[MT / 2][2], wa[NT / 2][2], wb[NT / 2][2];
+    const int sw = (r16 >> 1) & 7;
+    auto read_x = [&](mm_u32x4(*f)[2], int h, int s, auto part) {
+        const char *at = lds + (s & 1) * STAGE + h * XH + (wm * 8 * MT + r16) * 128;
+#pragma unroll
+        for (int i = from(part, MT); i < upto(part, MT); ++i)
+            f[i / 2][i % 2] = *(const mm_u32x4 *)(at + i / 2 * 2048 + (((4 * (i % 2) + g) ^ sw) << 4));
+    };
+    auto read_w = [&](mm_u32x4(*f)[2], int h, int s, auto part) {
+        const char *at = lds + (s & 1) * STAGE + 2 * XH + h * WH + (wn * 8 * NT + r16) * 128;
+#pragma unroll
+        for (int i = from(part, NT); i < upto(part, NT); ++i)
+            f[i / 2][i % 2] = *(const mm_u32x4 *)(at + i / 2 * 2048 + (((4 * (i % 2) + g) ^ sw) << 4));
+    };
+    auto multiply = [&](const mm_u32x4(*xf)[2], const mm_u32x4(*wf)[2], int mh, int nh, auto part) {
+        constexpr int PER = (MT / 2) * (NT / 2);
+#pragma unroll
+        for (int i = from(part, 2 * PER); i < upto(part, 2 * PER); ++i) {
+            const int k = i / PER, m = i % PER / (NT / 2), n = i % (NT / 2);
+            mm_f32x4 &c = acc[mh * (MT / 2) + m][nh * (NT / 2) + n];
+            if constexpr (ACC)
+                mma_acc<DT>(wf[n][k], xf[m][k], c);
+            else
+                c = mma<DT>(wf[n][k], xf[m][k], c);
+        }
+    };
+
+    // two steps' half tiles in the order of the phases, then X0 and W0 of the
+    // first into registers
+    constexpr Part<0, 1> all;
+    load_x(0, 0, No{}, all);
+    load_w(0, 0, No{}, all);
+    load_w(1, 0, No{}, all);
+    load_x(1, 0, No{}, all);
+    load_x(0, 1, No{}, all);
+    load_w(0, 1, No{}, all);
+    load_w(1, 1, No{}, all);
+    load_x(1, 1, No{}, all);
+    if (steps > 1)
+        wait_loads<3 * XI + 3 * WI>();
+    else
+        wait_loads<0>();
+    __builtin_amdgcn_s_barrier();
+    read_x(x0, 0, 0, all);
+    read_w(wa, 0, 0, all);
+    wait_loads<63>();
+    __builtin_amdgcn_s_barrier();
+    load_x(0, 2, No{}, all);
+
+    // A phase: its loads into LDS, its reads for the next phase and its products in
+    // four groups each, kept in this order.
+    auto phase = [&](auto &&load, auto &&read, auto &&mul) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        static_for<4>([&](auto i) {
+            constexpr Part<decltype(i)::value, 4> part;
+            load(part);
+            read(part);
+            mul(part);
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    // `whole`: steps s+1 .. s+3 are there and whole.  Towards the end the waits are
+    // for everything, since fewer loads follow than the counts assume.
+    auto step = [&](int s, mm_u32x4(*w0)[2], mm_u32x4(*w1)[2], auto whole) {
+        const bool next = whole || s + 1 < steps;
+        whole ? wait_loads<4 * XI + 2 * WI>() : wait_loads<0>();
+        phase([&](auto p) { load_w(0, s + 2, whole, p); }, [&](auto p) { read_w(w1, 1, s, p); },
+              [&](auto p) { multiply(x0, w0, 0, 0, p); });
+        whole ? wait_loads<3 * XI + 3 * WI>() : wait_loads<0>();
+        phase([&](auto p) { load_w(1, s + 2, whole, p); }, [&](auto p) { read_x(x1, 1, s, p); },
+              [&](auto p) { multiply(x0, w1, 0, 1, p); });
+        whole ? wait_loads<2 * XI + 4 * WI>() : wait_loads<0>();
+        phase([&](auto p) { load_x(1, s + 2, whole, p); }, [&](auto p) { if (next) read_x(x0, 0, s + 1, p); },
+              [&](auto p) { multiply(x1, w1, 1, 1, p); });
+        whole ? wait_loads<3 * XI + 3 * WI>() : wait_loads<0>();
+        phase([&](auto p) { load_x(0, s + 3, whole, p); }, [&](auto p) { if (next) read_w(w1, 0, s + 1, p); },
+              [&](auto p) { multiply(x1, w0, 1, 0, p); });
+    };
+    int s = 0;
+    for (; s + 4 < full; s += 2) {
+        step(s, wa, wb, Yes{});
+        step(s + 1, wb, wa, Yes{});
+    }
+    for (; s < steps; s += 2) {
+        step(s, wa, wb, No{});
+        if (s + 1 < steps) step(s + 1, wb, wa, No{});
+    }
+
+    if constexpr (ACC) settle<MT, NT>(acc);
+    const int col = col0 + wn * CW + g * 4 * NTC;
+    mm_f32x4 b[NT];
+    load_bias<DT, GATED, NT>(a, t.group, col, b);
+    // one row tile after the other: together they would not fit the registers
+    static_for<MT>([&](auto m) {
+        __builtin_amdgcn_sched_barrier(0);
+        finish_row<GATED, NT>(a, orow[wm * 16 * MT + m * 16 + r16], col, acc[m], b);
+    });
+}
+
+template <int DT, bool GATED, int MT, int NT>
+static void launch_tile(const MatmulArgs &a, const MatmulChoice &c, hipStream_t s) {
+    const unsigned blocks = (unsigned)(((int64_t)c.tiles_m * c.tiles_n + 7) / 8 * 8);
+    hipLaunchKernelGGL((matmul_tile_kernel<DT, GATED, MT, NT>), dim3(blocks), dim3(256), 0, s, a);
+}
+
+template <int DT>
+static void launch_dtype(const MatmulArgs &a, const MatmulChoice &c, hipStream_t s) {
+    switch (c.mt * 16 + c.nt) {
+#define MOE_TILE(M, N)                                                                                   \
+    case M * 16 + N:                                                                                     \
+        if constexpr (DT != MOE_DTYPE_F32 || M * N < 64)                                                 \
+            a.w_up ? launch_tile<DT, true, M, N>(a, c, s) : launch_tile<DT, false, M, N>(a, c, s);       \
+        break;
+        MOE_TILE(8, 8)
+        MOE_TILE(4, 4)
+#undef MOE_TILE
+    }
+}
+
+void launch_matmul_tile(int dtype, const MatmulArgs &a, const MatmulChoice &c, hipStream_t s) {
+    switch (dtype) {
+        case MOE_DTYPE_BF16: launch_dtype<MOE_DTYPE_BF16>(a, c, s); break;
+        case MOE_DTYPE_F16: launch_dtype<MOE_DTYPE_F16>(a, c, s); break;
+        default: launch_dtype<MOE_DTYPE_F32>(a, c, s); break;
+    }
+}
+
+}  // namespace moe
