@@ -39,11 +39,10 @@ __global__ __launch_bounds__(256) void matmul_tile64_kernel(MatmulArgs a) {
     for (int i = 0; i < 2; ++i) {
         const int row = tid / 8 + 32 * i;
         xp[i] = a.x + (int64_t)x_row(a, orow[row]) * a.x_stride;
-        // LDS row of w -> (wave column, tile j, row q of A) -> column: a lane
-        // of D then holds 4 NTC consecutive columns
+        // LDS row of w -> (wave column, tile j, row q of the operand) -> column
         const int j = (row & 31) >> 4, q = row & 15;
         const int jc = GATED ? 0 : j;
-        int col = col0 + (row >> 5) * CW + (q >> 2) * 4 * NTC + jc * 4 + (q & 3);
+        int col = col0 + (row >> 5) * CW + tile_col<NTC>(jc, q);
         if (col >= a.N) col = a.N - 1;
         const char *base = GATED && j ? a.w_up : a.w;
         wp[i] = base + (int64_t)t.group * a.w_group + (int64_t)col * a.w_row;
@@ -98,7 +97,7 @@ __global__ __launch_bounds__(256) void matmul_tile64_kernel(MatmulArgs a) {
         __syncthreads();
     }
 
-    const int col = col0 + wn * CW + g * 4 * NTC;
+    const int col = col0 + wn * CW + lane_col<NTC>(g);
     mm_f32x4 b[NT];
     load_bias<DT, GATED, NT>(a, t.group, col, b);
     static_for<MT>([&](auto m) { finish_row<GATED, NT>(a, orow[wm * 32 + m * 16 + r16], col, acc[m], b); });

@@ -59,7 +59,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs
     for (int i = 0; i < WI; ++i) {
         const int p = (wave * WI + i) * 8 + (lane >> 3);
         const int j = p / 16 % NT % NTC, ar = p & 15;
-        int col = p / (16 * NT) * CW + (ar >> 2) * 4 * NTC + j * 4 + (ar & 3);
+        int col = p / (16 * NT) * CW + tile_col<NTC>(j, ar);
         if (col0 + col >= a.N) col = a.N - 1 - col0;
         wo[i] = (uint32_t)col * (uint32_t)a.w_row + chunk_of(p) * 16;
     }
@@ -173,7 +173,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs
         if (s + 1 < steps) step(s + 1, xb, wb, xa, wa, No{});
     }
 
-    const int col = col0 + wn * CW + g * 4 * NTC;
+    const int col = col0 + wn * CW + lane_col<NTC>(g);
     mm_f32x4 b[NT];
     load_bias<DT, GATED, NT>(a, t.group, col, b);
     static_for<MT>([&](auto m) { finish_row<GATED, NT>(a, orow[wm * 16 * MT + m * 16 + r16], col, acc[m], b); });

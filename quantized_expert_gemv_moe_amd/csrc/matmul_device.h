@@ -144,33 +144,56 @@ __device__ __forceinline__ void store4(void *out, int64_t out_at, int out_dtype,
     }
 }
 
-// 4 NC consecutive columns of row o, in accumulators of four; 16-bit outputs go out
-// eight columns at a time where their addresses allow.
+// Columns of a wave's NC tiles of 16.  Which row of w stands in which place of the
+// operands is free, so they are dealt such that a lane (group g of 16) holds, of tiles
+// 2 q and 2 q + 1, the eight columns 32 q + 8 g .. + 7: the four groups' 16-byte stores of
+// a row are 64 bytes in a row.  (With all of a lane's columns adjacent, a store instruction
+// wrote 64 separate pieces, and the stores of a 256 x 256 tile took 4 us.)
+// A single tile keeps its order: group g holds columns 4 g .. + 3.
+template <int NC>
+__device__ __forceinline__ constexpr int tile_col(int j, int ar) {  // tile j, row ar of the operand
+    return NC == 1 ? ar : (j >> 1) * 32 + (ar >> 2) * 8 + (j & 1) * 4 + (ar & 3);
+}
+template <int NC>
+__device__ __forceinline__ constexpr int lane_col(int g) {  // first column of lane group g
+    return NC == 1 ? 4 * g : 8 * g;
+}
+template <int NC>
+__device__ __forceinline__ constexpr int acc_col(int n) {  // from there to accumulator n's
+    return (n >> 1) * 32 + (n & 1) * 4;
+}
+
+// A lane's columns of row o, from its first column `col`; 16-bit outputs go out eight
+// columns at a time where their addresses allow.
 template <int NC>
 __device__ __forceinline__ void store_row(const MatmulArgs &a, int o, int col, const mm_f32x4 *z) {
+    static_assert(NC == 1 || NC % 2 == 0, "tiles come in pairs");
     const int64_t out_at = (int64_t)o * a.out_stride, res_at = (int64_t)o * a.res_stride;
     if constexpr (NC % 2 == 0) {
-        if (a.vec_out == 2 && a.out_dtype != MOE_DTYPE_F32 && col + 4 * NC <= a.N) {
+        if (a.vec_out == 2 && a.out_dtype != MOE_DTYPE_F32 && a.N % 8 == 0) {
 #pragma unroll
             for (int n = 0; n < NC; n += 2) {
+                const int c = col + acc_col<NC>(n);
+                if (c >= a.N) continue;
                 mm_f32x4 v0 = z[n], v1 = z[n + 1];
                 if (a.residual) {
-                    v0 += load_value4(a.residual, res_at + col + 4 * n, a.res_dtype);
-                    v1 += load_value4(a.residual, res_at + col + 4 * n + 4, a.res_dtype);
+                    v0 += load_value4(a.residual, res_at + c, a.res_dtype);
+                    v1 += load_value4(a.residual, res_at + c + 4, a.res_dtype);
                 }
                 mm_u32x4 b;
                 b[0] = round_pair(v0[0], v0[1], a.out_dtype);
                 b[1] = round_pair(v0[2], v0[3], a.out_dtype);
                 b[2] = round_pair(v1[0], v1[1], a.out_dtype);
                 b[3] = round_pair(v1[2], v1[3], a.out_dtype);
-                *(mm_u32x4 *)((uint16_t *)a.out + out_at + col + 4 * n) = b;
+                *(mm_u32x4 *)((uint16_t *)a.out + out_at + c) = b;
             }
             return;
         }
     }
 #pragma unroll
     for (int n = 0; n < NC; ++n)
-        store4(a.out, out_at, a.out_dtype, a.residual, res_at, a.res_dtype, a.vec_out != 0, col + 4 * n, a.N, z[n]);
+        store4(a.out, out_at, a.out_dtype, a.residual, res_at, a.res_dtype, a.vec_out != 0, col + acc_col<NC>(n), a.N,
+               z[n]);
 }
 
 // ------------------------------------------------------------ activations
@@ -241,8 +264,8 @@ __device__ __forceinline__ void static_for(F &&f) {
 }
 
 // A row's accumulators to its stored values: bias, clip, f, gate, residual, one
-// rounding.  The lane holds columns col .. col + 4 NC - 1, gate in the first NC
-// accumulators and up in the others when gated.  b holds the columns' biases.
+// rounding.  The lane's first column is col; gate is in the first NC accumulators and
+// up in the others when gated.  b holds the columns' biases.
 template <bool GATED, int NT>
 __device__ __forceinline__ void finish_row(const MatmulArgs &a, int o, int col, mm_f32x4 *z, const mm_f32x4 *b) {
     constexpr int NC = GATED ? NT / 2 : NT;
@@ -275,7 +298,7 @@ __device__ __forceinline__ void load_bias(const MatmulArgs &a, int group, int co
         const char *p = (n < NC ? a.bias : a.bias_up) + (int64_t)group * a.bias_group;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int c = col + 4 * (n % NC) + r;
+            const int c = col + acc_col<NC>(n % NC) + r;
             b[n][r] = load_value(p, c < a.N ? c : a.N - 1, DT);
         }
     }

@@ -100,7 +100,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
             const int p = (wave * WI + i) * 8 + (lane >> 3);
             const int c = (lane & 7) ^ ((p >> 1) & 7);
             const int q = p % (8 * NT), j = (GATED ? 0 : h * (NT / 2)) + (q >> 4), ar = q & 15;
-            int col = p / (8 * NT) * CW + (ar >> 2) * 4 * NTC + j * 4 + (ar & 3);
+            int col = p / (8 * NT) * CW + tile_col<NTC>(j, ar);
             if (col0 + col >= a.N) col = a.N - 1 - col0;
             wo[h][i] = (uint32_t)col * (uint32_t)a.w_row + c * 16;
         }
@@ -174,17 +174,15 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
         }
     };
 
-    // two steps' half tiles in the order of the phases, then X0 and W0 of the
-    // first into registers
+    // two steps' half tiles in the order of their use, then X0 and W0 of the first
+    // into registers
     constexpr Part<0, 1> all;
-    load_x(0, 0, No{}, all);
-    load_w(0, 0, No{}, all);
-    load_w(1, 0, No{}, all);
-    load_x(1, 0, No{}, all);
-    load_x(0, 1, No{}, all);
-    load_w(0, 1, No{}, all);
-    load_w(1, 1, No{}, all);
-    load_x(1, 1, No{}, all);
+    for (int i = 0; i < 2; ++i) {
+        load_x(0, i, No{}, all);
+        load_w(0, i, No{}, all);
+        load_x(1, i, No{}, all);
+        load_w(1, i, No{}, all);
+    }
     if (steps > 1)
         wait_loads<3 * XI + 3 * WI>();
     else
@@ -192,43 +190,47 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
     __builtin_amdgcn_s_barrier();
     read_x(x0, 0, 0, all);
     read_w(wa, 0, 0, all);
-    wait_loads<63>();
-    __builtin_amdgcn_s_barrier();
-    load_x(0, 2, No{}, all);
 
-    // A phase: its loads into LDS, its reads for the next phase and its products in
-    // four groups each, kept in this order.
-    auto phase = [&](auto &&load, auto &&read, auto &&mul) {
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        static_for<4>([&](auto i) {
-            constexpr Part<decltype(i)::value, 4> part;
-            load(part);
-            read(part);
-            mul(part);
+    // A quadrant: its products in sixteen parts, after each of them one LDS read or load
+    // into LDS, kept in this order: a few instructions fit beside every matrix
+    // instruction, more in a row would leave the matrix core idle.  The last parts have
+    // no reads, so that they have arrived when the next barrier waits for them.
+    auto quadrant = [&](auto &&load, auto &&read, auto &&mul) {
+        static_for<16>([&](auto i) {
+            constexpr int I = decltype(i)::value;
+            constexpr int R = I - (I + 2) / 4;  // parts before this one without a load
+            mul(Part<I, 16>{});
+            if constexpr (I % 4 == 1)
+                load(Part<I / 4, 4>{});
+            else if constexpr (R < 8)
+                read(Part<R, 8>{});
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    // `whole`: steps s+1 .. s+3 are there and whole.  Towards the end the waits are
+    auto meet = [&] {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // `whole`: steps s+1 and s+2 are there and whole.  Towards the end the waits are
     // for everything, since fewer loads follow than the counts assume.
     auto step = [&](int s, mm_u32x4(*w0)[2], mm_u32x4(*w1)[2], auto whole) {
         const bool next = whole || s + 1 < steps;
-        whole ? wait_loads<4 * XI + 2 * WI>() : wait_loads<0>();
-        phase([&](auto p) { load_w(0, s + 2, whole, p); }, [&](auto p) { read_w(w1, 1, s, p); },
-              [&](auto p) { multiply(x0, w0, 0, 0, p); });
-        whole ? wait_loads<3 * XI + 3 * WI>() : wait_loads<0>();
-        phase([&](auto p) { load_w(1, s + 2, whole, p); }, [&](auto p) { read_x(x1, 1, s, p); },
-              [&](auto p) { multiply(x0, w1, 0, 1, p); });
-        whole ? wait_loads<2 * XI + 4 * WI>() : wait_loads<0>();
-        phase([&](auto p) { load_x(1, s + 2, whole, p); }, [&](auto p) { if (next) read_x(x0, 0, s + 1, p); },
-              [&](auto p) { multiply(x1, w1, 1, 1, p); });
-        whole ? wait_loads<3 * XI + 3 * WI>() : wait_loads<0>();
-        phase([&](auto p) { load_x(0, s + 3, whole, p); }, [&](auto p) { if (next) read_w(w1, 0, s + 1, p); },
-              [&](auto p) { multiply(x1, w0, 1, 0, p); });
+        whole ? wait_loads<2 * XI + 2 * WI>() : wait_loads<0>();
+        meet();
+        quadrant([&](auto p) { load_x(0, s + 2, whole, p); }, [&](auto p) { read_w(w1, 1, s, p); },
+                 [&](auto p) { multiply(x0, w0, 0, 0, p); });
+        quadrant([&](auto p) { load_w(0, s + 2, whole, p); }, [&](auto p) { read_x(x1, 1, s, p); },
+                 [&](auto p) { multiply(x0, w1, 0, 1, p); });
+        whole ? wait_loads<2 * XI + 2 * WI>() : wait_loads<0>();
+        meet();
+        quadrant([&](auto p) { load_x(1, s + 2, whole, p); }, [&](auto p) { if (next) read_x(x0, 0, s + 1, p); },
+                 [&](auto p) { multiply(x1, w1, 1, 1, p); });
+        quadrant([&](auto p) { load_w(1, s + 2, whole, p); }, [&](auto p) { if (next) read_w(w1, 0, s + 1, p); },
+                 [&](auto p) { multiply(x1, w0, 1, 0, p); });
     };
     int s = 0;
-    for (; s + 4 < full; s += 2) {
+    for (; s + 3 < full; s += 2) {
         step(s, wa, wb, Yes{});
         step(s + 1, wb, wa, Yes{});
     }
@@ -238,7 +240,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
     }
 
     if constexpr (ACC) settle<MT, NT>(acc);
-    const int col = col0 + wn * CW + g * 4 * NTC;
+    const int col = col0 + wn * CW + lane_col<NTC>(g);
     mm_f32x4 b[NT];
     load_bias<DT, GATED, NT>(a, t.group, col, b);
     // one row tile after the other: together they would not fit the registers
