@@ -80,7 +80,8 @@ static int64_t ragged_tiles(int64_t rows, int64_t groups, int64_t tile) {
 // against 8.8 of the 64 x 64 tile), then the tile grows with the work (1024 rows:
 // 64 x 128 13.8, 64 x 64 16.1, 128 x 128 24.1 us; 4096 rows: 128 x 128 37.1, 64 x
 // 128 43.1, 256 x 256 60.4 us; 8192 rows of K 8192, N 4096: 256 x 256 432 us, 128 x
-// 128 507 us).  fp32 steps take some three times as long: the matrix cores'
+// 128 507 us; 128 experts, top-8, 768 -> 2048: 16 tokens 32 x 64 42.6, 64 x 64 49.3
+// us, 512 tokens 32 x 64 99.6, 64 x 128 93.5 us).  fp32 steps take some three times as long: the matrix cores'
 // rate.
 struct Cost {
     MatmulKernel kernel;
@@ -88,6 +89,7 @@ struct Cost {
     double fixed, round, step, alone;
 };
 static const Cost kCosts[] = {
+    {kMatmulDeep, 1, 2, 3.3, 0.2, 0.13, 0.19},
     {kMatmulDeep, 2, 2, 3.3, 0.3, 0.20, 0.19}, {kMatmulDeep, 2, 4, 3.3, 0.5, 0.37, 0.27},
     {kMatmulTile, 4, 4, 3.3, 1.2, 0.53, 0.72}, {kMatmulTile, 8, 8, 3.3, 3.0, 1.70, 1.70},
     {kMatmulAny, 2, 2, 3.3, 0.5, 0.30, 0.90},  {kMatmulFew, 1, 0, 2.7, 0.0, 0.116, 0.116},

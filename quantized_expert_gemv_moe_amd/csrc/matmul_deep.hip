@@ -192,6 +192,7 @@ static void launch_dtype(const MatmulArgs &a, const MatmulChoice &c, hipStream_t
     case M * 16 + N:                                                                                          \
         a.w_up ? launch_deep<DT, true, WM, WN, MT, NT, S>(a, c, s) : launch_deep<DT, false, WM, WN, MT, NT, S>(a, c, s); \
         break;
+        MOE_DEEP(1, 2, 2, 2, 1, 2, 4)
         MOE_DEEP(2, 2, 2, 2, 2, 2, 4)
         MOE_DEEP(2, 4, 2, 4, 2, 2, 3)
 #undef MOE_DEEP
