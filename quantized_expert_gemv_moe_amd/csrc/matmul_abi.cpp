@@ -82,7 +82,9 @@ static int64_t ragged_tiles(int64_t rows, int64_t groups, int64_t tile) {
 // 128 43.1, 256 x 256 60.4 us; 8192 rows of K 8192, N 4096: 256 x 256 432 us, 128 x
 // 128 507 us; 128 experts, top-8, 768 -> 2048: 16 tokens 32 x 64 42.6, 64 x 64 49.3
 // us, 512 tokens 32 x 64 99.6, 64 x 128 93.5 us).  fp32 steps take some three times as long: the matrix cores'
-// rate.
+// rate.  Rows at odd addresses cost the kernel for few rows 2.3 times as much (16
+// rows, K 4096 and 4099, N 512: 9.5 and 19.5 us), so the register tile takes over
+// earlier (512 rows of 2047 by 2048: 16.5 us).
 struct Cost {
     MatmulKernel kernel;
     int mt, nt;
@@ -92,7 +94,7 @@ static const Cost kCosts[] = {
     {kMatmulDeep, 1, 2, 3.3, 0.2, 0.13, 0.19},
     {kMatmulDeep, 2, 2, 3.3, 0.3, 0.20, 0.19}, {kMatmulDeep, 2, 4, 3.3, 0.5, 0.37, 0.27},
     {kMatmulTile, 4, 4, 3.3, 1.2, 0.53, 0.72}, {kMatmulTile, 8, 8, 3.3, 3.0, 1.70, 1.70},
-    {kMatmulAny, 2, 2, 3.3, 0.5, 0.30, 0.90},  {kMatmulFew, 1, 0, 2.7, 0.0, 0.116, 0.116},
+    {kMatmulAny, 2, 2, 3.3, 0.5, 0.36, 0.40},  {kMatmulFew, 1, 0, 2.7, 0.0, 0.116, 0.116},
     {kMatmulFew, 2, 0, 2.7, 0.0, 0.170, 0.170}};
 
 MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bool is_aligned) {
@@ -117,6 +119,7 @@ MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bo
         double step = n <= 256 && k.alone > k.step ? k.alone : n <= 128 ? k.alone : k.step * rounds;
         if (f32 && !few) step *= 3;
         if (few && gated && k.mt == 2) step *= 1.4;
+        if (few && !is_aligned) step *= 2.3;
         const double time = k.fixed + k.round * rounds + step * steps;
         if (best.tiles_n == 0 || time < best_time) {
             best_time = time;
