@@ -25,7 +25,7 @@ __global__ __launch_bounds__(256) void matmul_tile64_kernel(MatmulArgs a) {
     __shared__ mm_u32x4 lds[2][BM + BW][8];
     __shared__ int orow[BM];
     MatmulTile t;
-    if (a.rows_mode == kRowsDense ? !dense_tile<8>(a, BM, &t) : !grouped_tile(a, BM, &t)) return;
+    if (!block_tile(a, BM, blockIdx.x, &t)) return;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid / 64;
     const int wm = wave & 1, wn = wave >> 1;
     const int g = lane >> 4, r16 = lane & 15;
@@ -127,11 +127,10 @@ static void launch_dtype(const MatmulArgs &a, const MatmulChoice &c, hipStream_t
 
 moe_status launch_matmul(const moe_linear_t *linear, const MatmulArgs &a, const MatmulChoice &c, void *workspace,
                          hipStream_t s) {
-    (void)workspace;
     if (c.kernel == kMatmulTile)
         launch_matmul_tile(linear->dtype, a, c, s);
     else if (c.kernel == kMatmulDeep)
-        launch_matmul_deep(linear->dtype, a, c, s);
+        launch_matmul_deep(linear->dtype, a, c, workspace, s);
     else if (c.kernel == kMatmulFew)
         launch_matmul_few(linear->dtype, a, c, s);
     else

@@ -93,9 +93,19 @@ struct Cost {
 static const Cost kCosts[] = {
     {kMatmulDeep, 1, 2, 3.3, 0.2, 0.13, 0.19},
     {kMatmulDeep, 2, 2, 3.3, 0.3, 0.20, 0.19}, {kMatmulDeep, 2, 4, 3.3, 0.5, 0.37, 0.27},
-    {kMatmulTile, 4, 4, 3.3, 1.2, 0.53, 0.72}, {kMatmulTile, 8, 8, 3.3, 3.0, 1.70, 1.70},
+    {kMatmulTile, 4, 4, 3.3, 1.2, 0.45, 0.54}, {kMatmulTile, 8, 8, 3.3, 3.0, 1.55, 1.10},
     {kMatmulAny, 2, 2, 3.3, 0.5, 0.36, 0.40},  {kMatmulFew, 1, 0, 2.7, 0.0, 0.116, 0.116},
     {kMatmulFew, 2, 0, 2.7, 0.0, 0.170, 0.170}};
+
+// K in stretches (kMatmulDeep): at most 16 of them, at most one tile's stretch for
+// each CU, and only where the model says that it gains more than the join costs: 3 us
+// on the device, and a second launch's 4 us on the host when calls are enqueued one by
+// one.  bf16, K 8192: 16 rows, N 512 17.7 (kernel for few rows) -> 8.1 us; 64 rows, N
+// 2048 24.6 -> 18.8 us; 16 rows, N 2048 17.7 either way, not split.
+constexpr int kMaxSplits = 16;
+constexpr int64_t kMaxSplitTiles = 256;
+constexpr double kJoinCost = 8.5;
+static size_t split_tile_bytes(const Cost &k) { return (size_t)(32 * k.mt) * (32 * k.nt) * sizeof(float); }
 
 MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bool is_aligned) {
     MatmulChoice best{};
@@ -120,15 +130,26 @@ MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bo
         if (f32 && !few) step *= 3;
         if (few && gated && k.mt == 2) step *= 1.4;
         if (few && !is_aligned) step *= 2.3;
+        if (few && rows <= 4) step *= 0.75;  // x is one line for all lanes of a step
         const double time = k.fixed + k.round * rounds + step * steps;
-        if (best.tiles_n == 0 || time < best_time) {
-            best_time = time;
+        auto take = [&](double t, int splits) {
+            if (best.tiles_n && t >= best_time) return;
+            best_time = t;
             best.kernel = k.kernel;
             best.mt = k.mt;
             best.nt = k.nt;
             best.tiles_m = (int)tm;
             best.tiles_n = (int)tn;
-        }
+            best.splits = splits;
+            best.workspace = splits == 1 ? 0 : (size_t)splits * tm * tn * split_tile_bytes(k);
+        };
+        take(time, 1);
+        if (k.kernel != kMatmulDeep) continue;
+        // K in stretches: a second launch and a pass over the parts, so it has to gain
+        // more than those cost
+        for (int splits = 2; splits <= kMaxSplits && tm * tn * splits <= kMaxSplitTiles && splits * 4 <= steps; splits *= 2)
+            take(k.fixed + k.round + k.alone * (f32 ? 3 : 1) * (tm * tn * splits > 128 ? 2 : 1) * steps / splits + kJoinCost,
+                 splits);
     }
     return best;  // tiles_n == 0: more workgroups than a launch takes
 }
@@ -272,12 +293,27 @@ extern "C" {
 
 moe_status moe_linear_check(const moe_linear_t *linear) { return moe::check_linear(linear); }
 
-// The size does not depend on x, so it covers the choice of either alignment.
+// Enough for every batch of up to max_rows rows, whatever the alignment of x: the
+// largest workspace of each tile, as its tiles grow with the rows until they are too
+// many to split.
 static size_t matmul_workspace(const moe_linear_t *linear, int32_t max_rows, bool grouped) {
-    if (moe::check_linear(linear) != MOE_OK || max_rows < 1) return 0;
-    const size_t a = moe::choose_matmul(linear, max_rows, grouped, true).workspace;
-    const size_t b = moe::choose_matmul(linear, max_rows, grouped, false).workspace;
-    return a > b ? a : b;
+    using namespace moe;
+    if (check_linear(linear) != MOE_OK || max_rows < 1) return 0;
+    const int64_t steps = tiles(linear->in_features * (int64_t)dtype_size(linear->dtype), 128);
+    size_t most = 0;
+    for (const Cost &k : kCosts) {
+        if (k.kernel != kMatmulDeep) continue;
+        const int64_t tile_rows = 32 * k.mt, tile_cols = (linear->w_up ? 16 : 32) * k.nt;
+        const int64_t tm = grouped ? ragged_tiles(max_rows, linear->n_groups, tile_rows) : tiles(max_rows, tile_rows);
+        const int64_t tn = tiles(linear->out_features, tile_cols);
+        int64_t splits = kMaxSplits;
+        while (splits > 1 && splits * 4 > steps) splits /= 2;
+        if (splits < 2 || 2 * tn > kMaxSplitTiles) continue;
+        const int64_t n = tm * tn * splits < kMaxSplitTiles ? tm * tn * splits : kMaxSplitTiles;
+        const size_t bytes = (size_t)n * split_tile_bytes(k);
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 size_t moe_matmul_workspace_size(const moe_linear_t *linear, int32_t max_rows) {

@@ -9,6 +9,12 @@
 //   reads the operands of step s + 1 into registers and multiplies those of step s.
 // So S - 1 steps of loads are in flight all the time, and reading LDS overlaps the
 // products.  The swizzle of the rows' chunks is that of the large tiles.
+//
+// Split: few tiles over a long K leave most CUs idle and take the time of one tile's
+// steps.  Then a tile's steps are cut into `splits` stretches, each a workgroup's, whose
+// accumulators go to the workspace as they are (1 KiB a wave and accumulator); a
+// second launch of the kernel adds them in the order of the stretches and finishes
+// the tile.  bf16 16 rows, K 8192, N 512: 25.7 -> 8.1 us; 64 rows, N 2048: 25.9 -> 18.8 us.
 #include <hip/hip_runtime.h>
 
 #include "matmul_device.h"
@@ -30,8 +36,13 @@ __device__ __forceinline__ void wait_stages(int left) {
     }
 }
 
-template <int DT, bool GATED, int WM, int WN, int MT, int NT, int S>
-__global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs a) {
+// What a launch does: whole tiles, a stretch of each tile's steps into the
+// workspace, or the stretches' sums out of it.
+enum DeepMode { kDeepWhole, kDeepPart, kDeepJoin };
+
+template <int DT, bool GATED, int WM, int WN, int MT, int NT, int S, DeepMode MODE>
+__global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs a, int splits,
+                                                                         mm_f32x4 *parts) {
     constexpr int BM = 16 * WM * MT, BW = 16 * WN * NT;
     constexpr int NTC = GATED ? NT / 2 : NT;  // column tiles of a wave
     constexpr int CW = NTC * 16;              // columns of a wave
@@ -40,12 +51,33 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs
     __shared__ __align__(1024) char lds[S * STAGE];
     __shared__ int orow[BM];
     MatmulTile t;
-    if (a.rows_mode == kRowsDense ? !dense_tile<8>(a, BM, &t) : !grouped_tile(a, BM, &t)) return;
+    const int blocks = MODE == kDeepPart ? gridDim.x / splits : gridDim.x;  // a multiple of 8
+    const int split = MODE == kDeepPart ? blockIdx.x / blocks : 0;
+    if (!block_tile(a, BM, blockIdx.x % blocks, &t)) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave % WM, wn = wave / WM;
     const int g = lane >> 4, r16 = lane & 15;
     const int col0 = t.tile_n * WN * CW;
+    mm_f32x4 acc[MT][NT];
+    // accumulator (m, n) of this wave for stretch k
+    auto part = [&](int k, int m, int n) -> mm_f32x4 & {
+        const int64_t tile = (int64_t)t.id * splits + k;
+        return parts[((tile * (WM * WN) + wave) * (MT * NT) + m * NT + n) * 64 + lane];
+    };
+    if constexpr (MODE == kDeepJoin) {
+        if (tid < BM) orow[tid] = out_row(a, t, t.row0 + tid);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) acc[m][n] = part(0, m, n);
+        for (int k = 1; k < splits; ++k)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[m][n] += part(k, m, n);
+        __syncthreads();
+    } else {
 
     // w first: its rows do not depend on the plan's slots
     const char *wbase = a.w + (int64_t)t.group * a.w_group + (int64_t)col0 * a.w_row;
@@ -63,7 +95,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs
         if (col0 + col >= a.N) col = a.N - 1 - col0;
         wo[i] = (uint32_t)col * (uint32_t)a.w_row + chunk_of(p) * 16;
     }
-    const int chunks = (a.K * kElemBytes<DT>) >> 4;  // of a row
+    int chunks = (a.K * kElemBytes<DT>) >> 4;  // of a row
+    if constexpr (MODE == kDeepPart) {  // of this stretch; it starts at the bases
+        const int all = (chunks + 7) >> 3;
+        const int s0 = (int)((int64_t)all * split / splits), s1 = (int)((int64_t)all * (split + 1) / splits);
+        chunks = (s1 * 8 < chunks ? s1 * 8 : chunks) - s0 * 8;
+        xbase += (int64_t)s0 * 128;
+        wbase += (int64_t)s0 * 128;
+        ubase += (int64_t)s0 * 128;
+    }
     const int full = chunks >> 3, steps = (chunks + 7) >> 3;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
 
@@ -113,7 +153,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs
         }
     }
 
-    mm_f32x4 acc[MT][NT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -172,7 +211,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs
         step(s, xa, wa, xb, wb, No{});
         if (s + 1 < steps) step(s + 1, xb, wb, xa, wa, No{});
     }
+    }
 
+    if constexpr (MODE == kDeepPart) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) part(split, m, n) = acc[m][n];
+        return;
+    }
     const int col = col0 + wn * CW + lane_col<NTC>(g);
     mm_f32x4 b[NT];
     load_bias<DT, GATED, NT>(a, t.group, col, b);
@@ -180,17 +227,28 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs
 }
 
 template <int DT, bool GATED, int WM, int WN, int MT, int NT, int S>
-static void launch_deep(const MatmulArgs &a, const MatmulChoice &c, hipStream_t s) {
+static void launch_deep(const MatmulArgs &a, const MatmulChoice &c, void *workspace, hipStream_t s) {
     const unsigned blocks = (unsigned)(((int64_t)c.tiles_m * c.tiles_n + 7) / 8 * 8);
-    hipLaunchKernelGGL((matmul_deep_kernel<DT, GATED, WM, WN, MT, NT, S>), dim3(blocks), dim3(64 * WM * WN), 0, s, a);
+    const dim3 block(64 * WM * WN);
+    mm_f32x4 *parts = (mm_f32x4 *)workspace;
+    if (c.splits == 1) {
+        hipLaunchKernelGGL((matmul_deep_kernel<DT, GATED, WM, WN, MT, NT, S, kDeepWhole>), dim3(blocks), block, 0, s, a,
+                           1, parts);
+        return;
+    }
+    hipLaunchKernelGGL((matmul_deep_kernel<DT, GATED, WM, WN, MT, NT, S, kDeepPart>), dim3(blocks * c.splits), block,
+                       0, s, a, c.splits, parts);
+    hipLaunchKernelGGL((matmul_deep_kernel<DT, GATED, WM, WN, MT, NT, S, kDeepJoin>), dim3(blocks), block, 0, s, a,
+                       c.splits, parts);
 }
 
 template <int DT>
-static void launch_dtype(const MatmulArgs &a, const MatmulChoice &c, hipStream_t s) {
+static void launch_dtype(const MatmulArgs &a, const MatmulChoice &c, void *ws, hipStream_t s) {
     switch (c.mt * 16 + c.nt) {
 #define MOE_DEEP(M, N, WM, WN, MT, NT, S)                                                                     \
     case M * 16 + N:                                                                                          \
-        a.w_up ? launch_deep<DT, true, WM, WN, MT, NT, S>(a, c, s) : launch_deep<DT, false, WM, WN, MT, NT, S>(a, c, s); \
+        a.w_up ? launch_deep<DT, true, WM, WN, MT, NT, S>(a, c, ws, s)                                        \
+               : launch_deep<DT, false, WM, WN, MT, NT, S>(a, c, ws, s);                                      \
         break;
         MOE_DEEP(1, 2, 2, 2, 1, 2, 4)
         MOE_DEEP(2, 2, 2, 2, 2, 2, 4)
@@ -199,11 +257,11 @@ static void launch_dtype(const MatmulArgs &a, const MatmulChoice &c, hipStream_t
     }
 }
 
-void launch_matmul_deep(int dtype, const MatmulArgs &a, const MatmulChoice &c, hipStream_t s) {
+void launch_matmul_deep(int dtype, const MatmulArgs &a, const MatmulChoice &c, void *ws, hipStream_t s) {
     switch (dtype) {
-        case MOE_DTYPE_BF16: launch_dtype<MOE_DTYPE_BF16>(a, c, s); break;
-        case MOE_DTYPE_F16: launch_dtype<MOE_DTYPE_F16>(a, c, s); break;
-        default: launch_dtype<MOE_DTYPE_F32>(a, c, s); break;
+        case MOE_DTYPE_BF16: launch_dtype<MOE_DTYPE_BF16>(a, c, ws, s); break;
+        case MOE_DTYPE_F16: launch_dtype<MOE_DTYPE_F16>(a, c, ws, s); break;
+        default: launch_dtype<MOE_DTYPE_F32>(a, c, ws, s); break;
     }
 }
 

@@ -309,6 +309,7 @@ __device__ __forceinline__ void load_bias(const MatmulArgs &a, int group, int co
 // place `first` and has `count` rows, and the tile_n-th block of columns.
 struct MatmulTile {
     int group, first, count, row0, tile_n;
+    int id;  // place in the order of tiles
 };
 
 // Workgroup ids are dealt to the XCDs round robin.  Each XCD takes one
@@ -324,13 +325,13 @@ __device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
 
 // Dense: blocks of GM row tiles, all columns of a block before the next.
 template <int GM>
-__device__ __forceinline__ bool dense_tile(const MatmulArgs &a, int BM, MatmulTile *t) {
-    const int64_t id = xcd_order(blockIdx.x, (int64_t)a.tiles_m * a.tiles_n);
+__device__ __forceinline__ bool dense_tile(const MatmulArgs &a, int BM, int block, MatmulTile *t) {
+    const int64_t id = xcd_order(block, (int64_t)a.tiles_m * a.tiles_n);
     if (id < 0) return false;
     const int per = GM * a.tiles_n;
     const int g = (int)(id / per), r = (int)(id - (int64_t)g * per);
     const int gm = a.tiles_m - g * GM < GM ? a.tiles_m - g * GM : GM;
-    *t = MatmulTile{0, 0, a.rows, (g * GM + r % gm) * BM, r / gm};
+    *t = MatmulTile{0, 0, a.rows, (g * GM + r % gm) * BM, r / gm, (int)id};
     return true;
 }
 
@@ -344,23 +345,27 @@ __device__ __forceinline__ bool group_record(const MatmulArgs &a, int u, int4 *r
 // column block before the next.  Every wave finds the tile by itself: each
 // lane sums the row tiles of a run of records, a wave scan places the runs,
 // and the lane whose run holds the tile finds its record.
-__device__ __forceinline__ bool grouped_tile(const MatmulArgs &a, int BM, MatmulTile *t) {
+__device__ __forceinline__ bool grouped_tile(const MatmulArgs &a, int BM, int block, MatmulTile *t) {
     const int lane = threadIdx.x & (kWave - 1);
     const int per = (a.n_records + kWave - 1) / kWave;
     const int u0 = lane * per;
     int mine = 0;
     for (int q = 0; q < per; ++q) {
         int4 r;
-        if (u0 + q < a.n_records && group_record(a, u0 + q, &r)) mine += (r.z + BM - 1) / BM;
+        if (u0 + q < a.n_records && group_record(a, u0 + q, &r)) mine += (r.z + BM - 1) / BM;  // at most 16 records
     }
+    // no plan of this call's slots has more than tiles_m row tiles; one that claims more
+    // (its records overlap) is cut there, so that tiles stay within the grid and the workspace
+    if (mine > a.tiles_m) mine = a.tiles_m;
     int incl = mine;
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
         const int v = __shfl_up(incl, d, kWave);
         if (lane >= d) incl += v;
     }
-    const int64_t total = (int64_t)__builtin_amdgcn_readlane(incl, kWave - 1) * a.tiles_n;
-    const int64_t id = xcd_order(blockIdx.x, total);
+    const int all = __builtin_amdgcn_readlane(incl, kWave - 1);
+    const int64_t total = (int64_t)(all < a.tiles_m ? all : a.tiles_m) * a.tiles_n;
+    const int64_t id = xcd_order(block, total);
     if (id < 0) return false;
     const int m = (int)(id / a.tiles_n);  // a row tile of the expert that holds the tile
     const int excl = incl - mine;
@@ -389,8 +394,13 @@ __device__ __forceinline__ bool grouped_tile(const MatmulArgs &a, int BM, Matmul
     const int nb = (count + BM - 1) / BM;
     const int local = (int)(id - (int64_t)at * a.tiles_n);
     *t = MatmulTile{__builtin_amdgcn_readfirstlane(r.x), __builtin_amdgcn_readfirstlane(r.y), count,
-                    (local % nb) * BM, local / nb};
+                    (local % nb) * BM, local / nb, (int)id};
     return true;
+}
+
+// The tile of workgroup number `block`, or false for one without.
+__device__ __forceinline__ bool block_tile(const MatmulArgs &a, int BM, int block, MatmulTile *t) {
+    return a.rows_mode == kRowsDense ? dense_tile<8>(a, BM, block, t) : grouped_tile(a, BM, block, t);
 }
 
 // Row of out for row i of a tile's group, or -1 for a row that is not stored: one past

@@ -46,6 +46,7 @@ struct MatmulChoice {
     int mt, nt;    // tile: 32 mt rows of x by 32 nt rows of w; kMatmulFew: 16 mt rows of x
     bool aligned;  // every row of x and w is whole, aligned 16-byte chunks
     int tiles_m, tiles_n;
+    int splits;    // kMatmulDeep: stretches of K
     size_t workspace;
 };
 
@@ -73,7 +74,8 @@ moe_status check_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx
 
 // The tile kernels that load straight into LDS (matmul_tile.hip).
 void launch_matmul_tile(int dtype, const MatmulArgs &args, const MatmulChoice &choice, hipStream_t stream);
-void launch_matmul_deep(int dtype, const MatmulArgs &args, const MatmulChoice &choice, hipStream_t stream);
+void launch_matmul_deep(int dtype, const MatmulArgs &args, const MatmulChoice &choice, void *workspace,
+                        hipStream_t stream);
 void launch_matmul_few(int dtype, const MatmulArgs &args, const MatmulChoice &choice, hipStream_t stream);
 moe_status launch_matmul(const moe_linear_t *linear, const MatmulArgs &args, const MatmulChoice &choice,
                          void *workspace, hipStream_t stream);

@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
     __shared__ __align__(1024) char lds[2 * STAGE];
     __shared__ int orow[BM];
     MatmulTile t;
-    if (a.rows_mode == kRowsDense ? !dense_tile<8>(a, BM, &t) : !grouped_tile(a, BM, &t)) return;
+    if (!block_tile(a, BM, blockIdx.x, &t)) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1, wn = wave >> 1;

@@ -101,6 +101,50 @@ def test_matmul_shapes(shape, gated, dtype):
     untouched()
 
 
+# few tiles over a long K: the inputs are split over workgroups through the workspace
+LONG = [(1, 16384, 64), (20, 8192, 96), (64, 8192, 512), (100, 4104, 130), (200, 8192, 300), (300, 16392, 64)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32], ids=["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_matmul_long_inputs(shape, gated, dtype):
+    """With a workspace full of NaN, exactly as large as asked for and between sentinels; one too
+    small is refused."""
+    rows, K, N = shape
+    log(f"[case] long {shape} gated={gated} {dtype}")
+    g = gen(rows + K + N)
+    lin = make_linear(g, None, N, K, dtype, gated, True, "silu", dtype)
+    x, res = normal(g, (rows, K), dtype), normal(g, (rows, N), F32)
+    need = moe.matmul_workspace_size(lin, rows)
+    assert need > 0
+    buf = torch.full((need // 4 + 128,), float("nan"), device="cuda")
+    buf[:64], buf[-64:] = SENTINEL, SENTINEL
+    ws = buf[64:-64]
+    out, untouched = out_view(rows, N, dtype, 0)
+    moe.matmul(lin, x, residual=res, out=out, workspace=ws)
+    again = moe.matmul(lin, x, residual=res)
+    torch.cuda.synchronize()
+    ref.check(out, *reference(lin, "silu", 0.0, x, res), name(shape=shape, gated=gated, dtype=dtype))
+    assert torch.equal(out, again)
+    assert bool((buf[:64] == SENTINEL).all()) and bool((buf[-64:] == SENTINEL).all()), "wrote outside the workspace"
+    untouched()
+    if torch.isnan(ws[0]):
+        return  # this shape took a kernel without a workspace
+    with pytest.raises(moe.MoeError) as e:
+        moe.matmul(lin, x, residual=res, out=out, workspace=ws[:64])
+    assert e.value.status == moe.MOE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("rows", ["token", "slot", "sorted"])
+@pytest.mark.parametrize("T,E,k", [(1, 2, 1), (3, 4, 2), (40, 3, 2), (100, 2, 1)])
+def test_grouped_long_inputs(T, E, k, rows):
+    idx = routing(np.random.default_rng(T), T, E, k)
+    for dtype, gated in ((BF16, True), (F16, False), (F32, False)):
+        log(f"[case] grouped long T={T} E={E} k={k} rows={rows} {dtype}")
+        check_grouped(idx, E, 8192, 64, dtype, gated, True, "silu", dtype, rows, tag=name(T=T, rows=rows, dtype=dtype))
+
+
 @pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "gelu_tanh"])
 @pytest.mark.parametrize("out_dtype", [BF16, F16, F32], ids=["obf16", "ofp16", "ofp32"])
 @pytest.mark.parametrize("rows", [3, 70])
@@ -354,6 +398,25 @@ def test_grouped_ignores_a_malformed_plan():
             stays = (out == torch.tensor(SENTINEL, dtype=BF16, device="cuda")).all(dim=1)
             ref.check(out[~stays], full[~stays], tol[~stays], breakage)
             assert bool(stays.any()), breakage
+
+
+@pytest.mark.parametrize("K", [64, 8192])
+def test_grouped_keeps_to_its_workspace_when_records_overlap(K):
+    """A plan whose records all claim every slot needs more tiles than any real plan of that
+    many slots: what does not fit is dropped, nothing outside out and the workspace is written."""
+    g = gen(4)
+    E, n, N = 8, 70, 64
+    lin = make_linear(g, E, N, K, BF16, False, False, "none", BF16)
+    plan = moe.expert_plan(torch.arange(n, dtype=torch.int32, device="cuda").view(n, 1) % E, E)
+    plan.work[:, 1], plan.work[:, 2] = 0, n
+    x = normal(g, (n, K), BF16)
+    need = max(moe.grouped_workspace_size(lin, n), 256)
+    buf = torch.full((need // 4 + 128,), SENTINEL, device="cuda")
+    out, untouched = out_view(n, N, BF16, 0)
+    moe.grouped_matmul(lin, x, plan, n, rows="slot", out=out, workspace=buf[64:-64])
+    torch.cuda.synchronize()
+    untouched()
+    assert bool((buf[:64] == SENTINEL).all()) and bool((buf[-64:] == SENTINEL).all())
 
 
 def test_grouped_same_rows_as_one_matmul():
