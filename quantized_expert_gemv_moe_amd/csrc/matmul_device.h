@@ -170,7 +170,7 @@ __device__ __forceinline__ void store_row(const MatmulArgs &a, int o, int col, c
     static_assert(NC == 1 || NC % 2 == 0, "tiles come in pairs");
     const int64_t out_at = (int64_t)o * a.out_stride, res_at = (int64_t)o * a.res_stride;
     if constexpr (NC % 2 == 0) {
-        if (a.vec_out == 2 && a.out_dtype != MOE_DTYPE_F32 && a.N % 8 == 0) {
+        if (a.vec_out >= 2 && a.out_dtype != MOE_DTYPE_F32 && a.N % 8 == 0) {
 #pragma unroll
             for (int n = 0; n < NC; n += 2) {
                 const int c = col + acc_col<NC>(n);
@@ -223,8 +223,17 @@ __device__ __forceinline__ float clip(float z, float limit) {  // NaN stays NaN
     return z > limit ? limit : (z < -limit ? -limit : z);
 }
 
-// z / (1 + exp(-z)); the reciprocal is good to 1 ulp.
-__device__ __forceinline__ float silu(float z) { return z * __builtin_amdgcn_rcpf(1.0f + expf(-z)); }
+// z / (1 + exp(-a)).  The exponential is 2 to the rounded product -a log2(e): off by |a|
+// 2^-24 relative where it counts, which is below the rounding of 16-bit outputs and
+// next to that of the products' sums in fp32.  The reciprocal is good to 1 ulp.
+__device__ __forceinline__ float sigmoid_mul(float z, float a) {
+    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.4426950408889634f));
+}
+__device__ __forceinline__ float silu(float z) { return sigmoid_mul(z, z); }
+// 0.5 (1 + tanh(b)) = 1 / (1 + exp(-2 b)): no cancellation
+__device__ __forceinline__ float gelu_tanh(float z) {
+    return sigmoid_mul(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
+}
 
 // f over N accumulators.  The function is uniform over the launch, so the choice
 // is made once for all of them and not per element.
@@ -242,8 +251,7 @@ __device__ __forceinline__ void apply_fn(mm_f32x4 *z, int fn) {
         case MOE_FN_RELU: MOE_APPLY(v < 0.f ? 0.f : v);
         case MOE_FN_SILU: MOE_APPLY(silu(v));
         case MOE_FN_GELU: MOE_APPLY(gelu_normal(v));
-        case MOE_FN_GELU_TANH:  // 0.5 (1 + tanh a) = 1 / (1 + exp(-2 a)): no cancellation
-            MOE_APPLY(v * __builtin_amdgcn_rcpf(1.0f + expf(-1.5957691216057308f * (v + 0.044715f * v * v * v))));
+        case MOE_FN_GELU_TANH: MOE_APPLY(gelu_tanh(v));
         default: break;
     }
 #undef MOE_APPLY

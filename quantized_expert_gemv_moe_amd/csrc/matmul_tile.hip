@@ -240,13 +240,91 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
     }
 
     if constexpr (ACC) settle<MT, NT>(acc);
+    // The results.  Code that runs once a tile comes out of the caches slowly, and
+    // branches over the forms not taken made up a third of a tile's fixed 23 us;
+    // so the usual outputs (whole, aligned columns of the weights' 16-bit type) have a
+    // straight path for each function, everything else one compact loop.
     const int col = col0 + wn * CW + lane_col<NTC>(g);
-    mm_f32x4 b[NT];
-    load_bias<DT, GATED, NT>(a, t.group, col, b);
-    // one row tile after the other: together they would not fit the registers
-    static_for<MT>([&](auto m) {
-        __builtin_amdgcn_sched_barrier(0);
-        finish_row<GATED, NT>(a, orow[wm * 16 * MT + m * 16 + r16], col, acc[m], b);
+    auto row_of = [&](int m) { return wm * 16 * MT + m * 16 + r16; };
+    if constexpr (DT != MOE_DTYPE_F32) {
+        if (a.vec_out == 3 && a.out_dtype == DT && col0 + 2 * CW <= a.N) {
+            mm_f32x4 b[NT];
+            load_bias<DT, GATED, NT>(a, t.group, col, b);
+            auto straight = [&](auto f, auto has_residual) __attribute__((always_inline)) {
+                // a row's residual is fetched while the row before is finished
+                mm_u32x4 res[2][has_residual ? NTC / 2 : 1];
+                auto fetch = [&](auto m) __attribute__((always_inline)) {
+                    if constexpr (has_residual) {
+                        const int o = orow[row_of(m)];
+                        const uint16_t *p = (const uint16_t *)a.residual + (int64_t)(o < 0 ? 0 : o) * a.res_stride + col;
+#pragma unroll
+                        for (int n = 0; n < NTC; n += 2) res[m % 2][n / 2] = *(const mm_u32x4 *)(p + acc_col<NTC>(n));
+                    }
+                };
+                fetch(Index<0>{});
+                static_for<MT>([&](auto m) __attribute__((always_inline)) {
+                    __builtin_amdgcn_sched_barrier(0);  // all rows together would not fit the registers
+                    if constexpr (m + 1 < MT) fetch(Index<m + 1>{});
+                    mm_f32x4 *z = acc[m];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) z[n] += b[n];
+                    if (a.clamp > 0.f) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r) z[n][r] = clip(z[n][r], a.clamp);
+                    }
+                    const int o = orow[row_of(m)];
+                    uint16_t *p = (uint16_t *)a.out + (int64_t)(o < 0 ? 0 : o) * a.out_stride + col;
+#pragma unroll
+                    for (int n = 0; n < NTC; n += 2) {
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            v[i] = f(z[n + i / 4][i % 4]);
+                            if constexpr (GATED) v[i] *= z[n + NTC + i / 4][i % 4];
+                            if constexpr (has_residual) {
+                                const uint32_t w = res[m % 2][n / 2][i / 2];
+                                const uint16_t h = (uint16_t)(i % 2 ? w >> 16 : w);
+                                v[i] += DT == MOE_DTYPE_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+                            }
+                        }
+                        const mm_u32x4 w = {round_pair(v[0], v[1], DT), round_pair(v[2], v[3], DT),
+                                            round_pair(v[4], v[5], DT), round_pair(v[6], v[7], DT)};
+                        if (o >= 0) *(mm_u32x4 *)(p + acc_col<NTC>(n)) = w;
+                    }
+                });
+            };
+            auto either = [&](auto f) __attribute__((always_inline)) {
+                a.residual ? straight(f, Yes{}) : straight(f, No{});
+            };
+            switch (a.fn) {
+                case MOE_FN_NONE: either([](float z) { return z; }); return;
+                case MOE_FN_SILU: either([](float z) { return silu(z); }); return;
+                case MOE_FN_GELU_TANH: either([](float z) { return gelu_tanh(z); }); return;
+                default: break;
+            }
+        }
+    }
+    // Through the wave's part of LDS, four row tiles at a time, one accumulator of
+    // every lane after the other.
+    constexpr int PASS = 4;
+    static_assert(PASS * NT * 1024 * 4 <= 2 * STAGE && MT % PASS == 0, "a wave's part holds a pass");
+    mm_f32x4 *mine = (mm_f32x4 *)lds + wave * (PASS * NT * 64) + lane;
+    __syncthreads();  // every wave has read its operands
+    static_for<MT / PASS>([&](auto pass) __attribute__((always_inline)) {
+        static_for<PASS * NT>([&](auto i) __attribute__((always_inline)) {
+            mine[i * 64] = acc[pass * PASS + i / NT][i % NT];
+        });
+#pragma unroll 1
+        for (int i = 0; i < PASS * NTC; ++i) {
+            const int m = i / NTC, n = i % NTC, c = col + acc_col<NTC>(n);
+            mm_f32x4 z[GATED ? 2 : 1], b[GATED ? 2 : 1];
+            z[0] = mine[(m * NT + n) * 64];
+            if constexpr (GATED) z[1] = mine[(m * NT + n + NTC) * 64];
+            load_bias<DT, GATED, GATED ? 2 : 1>(a, t.group, c, b);
+            finish_row<GATED, GATED ? 2 : 1>(a, orow[row_of(pass * PASS + m)], c, z, b);
+        }
     });
 }
 
