@@ -719,7 +719,7 @@ def grouped_matmul(linear: Linear, x: torch.Tensor, plan: Plan, n_slots: int, to
     row per token, slot s reads row s // top_k), "slot" (x has a row per slot) or "sorted"
     (rows of x and out lie grouped by expert, in the plan's order).  Rows of slots that the
     plan does not list are left as they are (unset when out is allocated here)."""
-    device = linear.device
+    device, n_slots, top_k = linear.device, int(n_slots), int(top_k)
     if stream is not None or _get_device() != device.index:
         return _on(device, stream,
                    lambda handle: _grouped(linear, x, plan, n_slots, top_k, rows, out, workspace, handle))
@@ -798,7 +798,7 @@ def _combine(y, idx, w, n_experts, residual, out, out_dtype, handle):
     if (out.shape != (B, H) or out.device != device or out_type is None or not out.is_contiguous()
             or (out_dtype is not None and out.dtype is not out_dtype)):
         _refuse("out", out, B, H, f"contiguous {out_dtype or 'bf16, fp16 or fp32'}", device)
-    st = lib().moe_combine(y.data_ptr(), y_type, idx.data_ptr(), w.data_ptr(), B, H, k, n_experts, res, res_type,
+    st = lib().moe_combine(y.data_ptr(), y_type, idx.data_ptr(), w.data_ptr(), B, H, k, int(n_experts), res, res_type,
                            out.data_ptr(), out_type, handle)
     if st:
         raise MoeError(st, "moe_combine")

@@ -78,139 +78,136 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(MatmulArgs
                 for (int n = 0; n < NT; ++n) acc[m][n] += part(k, m, n);
         __syncthreads();
     } else {
-
-    // w first: its rows do not depend on the plan's slots
-    const char *wbase = a.w + (int64_t)t.group * a.w_group + (int64_t)col0 * a.w_row;
-    const char *ubase = GATED ? a.w_up + (int64_t)t.group * a.w_group + (int64_t)col0 * a.w_row : wbase;
-    const bool gathered = a.rows_mode == MOE_ROWS_TOKEN || a.rows_mode == MOE_ROWS_SLOT;
-    const char *xbase = gathered ? a.x : a.x + (int64_t)(t.first + t.row0) * a.x_stride;
-    uint32_t xo[XI], wo[WI];
-    auto chunk_of = [&](int p) { return (lane & 7) ^ ((p >> 1) & 7); };
-    auto is_up = [&](int i) { return GATED && ((wave * WI + i) * 8 / 16) % NT >= NTC; };  // per 16 rows
-#pragma unroll
-    for (int i = 0; i < WI; ++i) {
-        const int p = (wave * WI + i) * 8 + (lane >> 3);
-        const int j = p / 16 % NT % NTC, ar = p & 15;
-        int col = p / (16 * NT) * CW + tile_col<NTC>(j, ar);
-        if (col0 + col >= a.N) col = a.N - 1 - col0;
-        wo[i] = (uint32_t)col * (uint32_t)a.w_row + chunk_of(p) * 16;
-    }
-    int chunks = (a.K * kElemBytes<DT>) >> 4;  // of a row
-    if constexpr (MODE == kDeepPart) {  // of this stretch; it starts at the bases
-        const int all = (chunks + 7) >> 3;
-        const int s0 = (int)((int64_t)all * split / splits), s1 = (int)((int64_t)all * (split + 1) / splits);
-        chunks = (s1 * 8 < chunks ? s1 * 8 : chunks) - s0 * 8;
-        xbase += (int64_t)s0 * 128;
-        wbase += (int64_t)s0 * 128;
-        ubase += (int64_t)s0 * 128;
-    }
-    const int full = chunks >> 3, steps = (chunks + 7) >> 3;
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-
-    auto load_w = [&](int s, int slot, auto whole) {
-        const uint32_t at = lds0 + slot * STAGE + XB + wave * WI * 1024;
+        // w first: its rows do not depend on the plan's slots
+        const char *wbase = a.w + (int64_t)t.group * a.w_group + (int64_t)col0 * a.w_row;
+        const char *ubase = GATED ? a.w_up + (int64_t)t.group * a.w_group + (int64_t)col0 * a.w_row : wbase;
+        const bool gathered = a.rows_mode == MOE_ROWS_TOKEN || a.rows_mode == MOE_ROWS_SLOT;
+        const char *xbase = gathered ? a.x : a.x + (int64_t)(t.first + t.row0) * a.x_stride;
+        uint32_t xo[XI], wo[WI];
+        auto chunk_of = [&](int p) { return (lane & 7) ^ ((p >> 1) & 7); };
+        auto is_up = [&](int i) { return GATED && ((wave * WI + i) * 8 / 16) % NT >= NTC; };  // per 16 rows
 #pragma unroll
         for (int i = 0; i < WI; ++i) {
-            const char *b = (is_up(i) ? ubase : wbase) + (int64_t)s * 128;
-            if (whole || s < full)
-                dma16(at + i * 1024, b, wo[i]);
-            else  // the last, partial step: zeros past the row's end
-                dma16(at + i * 1024, s * 8 + chunk_of((wave * WI + i) * 8 + (lane >> 3)) < chunks
-                                         ? b + wo[i] : (const char *)&kZeroChunk);
+            const int p = (wave * WI + i) * 8 + (lane >> 3);
+            const int j = p / 16 % NT % NTC, ar = p & 15;
+            int col = p / (16 * NT) * CW + tile_col<NTC>(j, ar);
+            if (col0 + col >= a.N) col = a.N - 1 - col0;
+            wo[i] = (uint32_t)col * (uint32_t)a.w_row + chunk_of(p) * 16;
         }
-    };
-    auto load_x = [&](int s, int slot, auto whole) {
-        const uint32_t at = lds0 + slot * STAGE + wave * XI * 1024;
-        const char *b = xbase + (int64_t)s * 128;
+        int chunks = (a.K * kElemBytes<DT>) >> 4;  // of a row
+        if constexpr (MODE == kDeepPart) {  // of this stretch; it starts at the bases
+            const int all = (chunks + 7) >> 3;
+            const int s0 = (int)((int64_t)all * split / splits), s1 = (int)((int64_t)all * (split + 1) / splits);
+            chunks = (s1 * 8 < chunks ? s1 * 8 : chunks) - s0 * 8;
+            xbase += (int64_t)s0 * 128;
+            wbase += (int64_t)s0 * 128;
+            ubase += (int64_t)s0 * 128;
+        }
+        const int full = chunks >> 3, steps = (chunks + 7) >> 3;
+        const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+
+        auto load_w = [&](int s, int slot, auto whole) {
+            const uint32_t at = lds0 + slot * STAGE + XB + wave * WI * 1024;
+#pragma unroll
+            for (int i = 0; i < WI; ++i) {
+                const char *b = (is_up(i) ? ubase : wbase) + (int64_t)s * 128;
+                if (whole || s < full)
+                    dma16(at + i * 1024, b, wo[i]);
+                else  // the last, partial step: zeros past the row's end
+                    dma16(at + i * 1024, s * 8 + chunk_of((wave * WI + i) * 8 + (lane >> 3)) < chunks
+                                             ? b + wo[i] : (const char *)&kZeroChunk);
+            }
+        };
+        auto load_x = [&](int s, int slot, auto whole) {
+            const uint32_t at = lds0 + slot * STAGE + wave * XI * 1024;
+            const char *b = xbase + (int64_t)s * 128;
+#pragma unroll
+            for (int i = 0; i < XI; ++i) {
+                if (whole || s < full)
+                    dma16(at + i * 1024, b, xo[i]);
+                else
+                    dma16(at + i * 1024, s * 8 + chunk_of((wave * XI + i) * 8 + (lane >> 3)) < chunks
+                                             ? b + xo[i] : (const char *)&kZeroChunk);
+            }
+        };
+        // the stages' loads; the rows of x are looked up behind those of w
+        if (tid < BM) orow[tid] = out_row(a, t, t.row0 + tid);
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < XI; ++i) {
-            if (whole || s < full)
-                dma16(at + i * 1024, b, xo[i]);
-            else
-                dma16(at + i * 1024, s * 8 + chunk_of((wave * XI + i) * 8 + (lane >> 3)) < chunks
-                                         ? b + xo[i] : (const char *)&kZeroChunk);
+            const int p = (wave * XI + i) * 8 + (lane >> 3);
+            const int xr = gathered ? x_row(a, orow[p]) : (t.row0 + p < t.count ? p : 0);
+            xo[i] = (uint32_t)xr * (uint32_t)a.x_stride + chunk_of(p) * 16;
         }
-    };
-    // the stages' loads; the rows of x are looked up behind those of w
-    if (tid < BM) orow[tid] = out_row(a, t, t.row0 + tid);
-    __syncthreads();
+        if (S <= full) {
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
-        const int p = (wave * XI + i) * 8 + (lane >> 3);
-        const int xr = gathered ? x_row(a, orow[p]) : (t.row0 + p < t.count ? p : 0);
-        xo[i] = (uint32_t)xr * (uint32_t)a.x_stride + chunk_of(p) * 16;
-    }
-    if (S <= full) {
-#pragma unroll
-        for (int s = 0; s < S; ++s) {
-            load_w(s, s, Yes{});
-            load_x(s, s, Yes{});
+            for (int s = 0; s < S; ++s) {
+                load_w(s, s, Yes{});
+                load_x(s, s, Yes{});
+            }
+        } else {
+            for (int s = 0; s < steps && s < S; ++s) {
+                load_w(s, s, No{});
+                load_x(s, s, No{});
+            }
         }
-    } else {
-        for (int s = 0; s < steps && s < S; ++s) {
-            load_w(s, s, No{});
-            load_x(s, s, No{});
-        }
-    }
 
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[m][n] = mm_f32x4{0.f, 0.f, 0.f, 0.f};
-    const int sw = (r16 >> 1) & 7;
-    auto read = [&](mm_u32x4(*xf)[2], mm_u32x4(*wf)[2], int slot) {
-        const char *xs = lds + slot * STAGE + (wm * 16 * MT + r16) * 128;
-        const char *ws = lds + slot * STAGE + XB + (wn * 16 * NT + r16) * 128;
+            for (int n = 0; n < NT; ++n) acc[m][n] = mm_f32x4{0.f, 0.f, 0.f, 0.f};
+        const int sw = (r16 >> 1) & 7;
+        auto read = [&](mm_u32x4(*xf)[2], mm_u32x4(*wf)[2], int slot) {
+            const char *xs = lds + slot * STAGE + (wm * 16 * MT + r16) * 128;
+            const char *ws = lds + slot * STAGE + XB + (wn * 16 * NT + r16) * 128;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+            for (int k = 0; k < 2; ++k) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) xf[m][k] = *(const mm_u32x4 *)(xs + m * 2048 + (((4 * k + g) ^ sw) << 4));
+                for (int m = 0; m < MT; ++m) xf[m][k] = *(const mm_u32x4 *)(xs + m * 2048 + (((4 * k + g) ^ sw) << 4));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) wf[n][k] = *(const mm_u32x4 *)(ws + n * 2048 + (((4 * k + g) ^ sw) << 4));
+                for (int n = 0; n < NT; ++n) wf[n][k] = *(const mm_u32x4 *)(ws + n * 2048 + (((4 * k + g) ^ sw) << 4));
+            }
+        };
+        auto multiply = [&](const mm_u32x4(*xf)[2], const mm_u32x4(*wf)[2]) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) acc[m][n] = mma<DT>(wf[n][k], xf[m][k], acc[m][n]);
+        };
+        mm_u32x4 xa[MT][2], wa[NT][2], xb[MT][2], wb[NT][2];
+        constexpr int L = XI + WI;
+        wait_stages<L, S - 1>(steps - 1);
+        meet();
+        read(xa, wa, 0);
+        int slot = 0;  // of step s
+        // `whole`: step s + S is there and whole, so nothing here branches (a step is
+        // short: the branches of the general form cost more than its products)
+        auto step = [&](int s, mm_u32x4(*x0)[2], mm_u32x4(*w0)[2], mm_u32x4(*x1)[2], mm_u32x4(*w1)[2], auto whole) {
+            if constexpr (whole)
+                wait_loads<L * (S - 2)>();
+            else
+                wait_stages<L, S - 2>(steps - 2 - s);
+            meet();
+            const int next = slot + 1 == S ? 0 : slot + 1;
+            if (whole || s + S < steps) {
+                load_w(s + S, slot, whole);
+                load_x(s + S, slot, whole);
+            }
+            if (whole || s + 1 < steps) read(x1, w1, next);
+            multiply(x0, w0);
+            slot = next;
+        };
+        int s = 0;
+        for (; s + 1 + S < full; s += 2) {
+            step(s, xa, wa, xb, wb, Yes{});
+            step(s + 1, xb, wb, xa, wa, Yes{});
         }
-    };
-    auto multiply = [&](const mm_u32x4(*xf)[2], const mm_u32x4(*wf)[2]) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int n = 0; n < NT; ++n) acc[m][n] = mma<DT>(wf[n][k], xf[m][k], acc[m][n]);
-    };
-    mm_u32x4 xa[MT][2], wa[NT][2], xb[MT][2], wb[NT][2];
-    constexpr int L = XI + WI;
-    wait_stages<L, S - 1>(steps - 1);
-    __builtin_amdgcn_s_barrier();
-    read(xa, wa, 0);
-    int slot = 0;  // of step s
-    // `whole`: step s + S is there and whole, so nothing here branches (a step is
-    // short: the branches of the general form cost more than its products)
-    auto step = [&](int s, mm_u32x4(*x0)[2], mm_u32x4(*w0)[2], mm_u32x4(*x1)[2], mm_u32x4(*w1)[2], auto whole) {
-        if constexpr (whole)
-            wait_loads<L * (S - 2)>();
-        else
-            wait_stages<L, S - 2>(steps - 2 - s);
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
-        const int next = slot + 1 == S ? 0 : slot + 1;
-        if (whole || s + S < steps) {
-            load_w(s + S, slot, whole);
-            load_x(s + S, slot, whole);
+        for (; s < steps; s += 2) {
+            step(s, xa, wa, xb, wb, No{});
+            if (s + 1 < steps) step(s + 1, xb, wb, xa, wa, No{});
         }
-        if (whole || s + 1 < steps) read(x1, w1, next);
-        multiply(x0, w0);
-        slot = next;
-    };
-    int s = 0;
-    for (; s + 1 + S < full; s += 2) {
-        step(s, xa, wa, xb, wb, Yes{});
-        step(s + 1, xb, wb, xa, wa, Yes{});
-    }
-    for (; s < steps; s += 2) {
-        step(s, xa, wa, xb, wb, No{});
-        if (s + 1 < steps) step(s + 1, xb, wb, xa, wa, No{});
-    }
     }
 
     if constexpr (MODE == kDeepPart) {

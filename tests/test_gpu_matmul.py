@@ -267,6 +267,92 @@ def test_matmul_is_reproducible_and_rows_keep_to_themselves(rows, K, N):
     assert torch.equal(a[rows // 3].view(torch.int16), c[rows // 3].view(torch.int16))
 
 
+# sizes at which the large tiles run, with ends inside a tile and a step
+LARGE = [(4096, 520, 4096), (4096, 512, 4000), (4100, 512, 4104), (2048, 2048, 2048), (3000, 4096, 1100)]
+LARGE_FORMS = [  # gated, function, out type (None: the weights'), residual type (0: the weights'), clamp
+    (False, "none", None, 0, 0.0), (False, "silu", None, None, 0.0), (False, "gelu_tanh", None, 0, 1.5),
+    (False, "gelu", None, None, 0.0), (False, "relu", None, F32, 0.0), (False, "none", F32, F32, 0.0),
+    (True, "silu", None, None, 0.0), (True, "gelu_tanh", None, 0, 0.8), (True, "silu", F32, None, 0.0)]
+
+
+@pytest.mark.parametrize("form", LARGE_FORMS, ids=lambda f: "-".join(str(v).replace("torch.", "") for v in f))
+@pytest.mark.parametrize("shape", LARGE, ids=lambda s: "x".join(map(str, s)))
+def test_matmul_large_tiles(shape, form):
+    rows, K, N = shape
+    gated, act, out_dtype, res_dtype, clamp = form
+    for dtype in (BF16, F16):
+        log(f"[case] large {shape} {form} {dtype}")
+        g = gen(rows + K)
+        od = out_dtype or dtype
+        lin = make_linear(g, None, N, K, dtype, gated, True, act, od, clamp)
+        x = normal(g, (rows, K), dtype)
+        res = None if res_dtype is None else normal(g, (rows, N), res_dtype or dtype)
+        out, untouched = out_view(rows, N, od, 0)
+        moe.matmul(lin, x, residual=res, out=out)
+        torch.cuda.synchronize()
+        ref.check(out, *reference(lin, act, clamp, x, res), name(shape=shape, form=form, dtype=dtype))
+        untouched()
+        if res is not None and res.dtype == od:  # onto its residual, in place
+            moe.matmul(lin, x, residual=res, out=res)
+            torch.cuda.synchronize()
+            assert torch.equal(res, out)
+
+
+@pytest.mark.parametrize("pad,offset", [(4, 0), (8, 0), (0, 4), (1, 0), (0, 1)])
+def test_matmul_large_tiles_into_strided_rows(pad, offset):
+    g = gen(14)
+    rows, K, N = 4096, 512, 4096
+    lin = make_linear(g, None, N, K, BF16, False, False, "silu", BF16)
+    x = normal(g, (rows, K), BF16)
+    res = strided(g, rows, N, BF16, pad, offset=offset)
+    out, untouched = out_view(rows, N, BF16, pad, offset=offset)
+    moe.matmul(lin, x, residual=res, out=out)
+    torch.cuda.synchronize()
+    ref.check(out, *reference(lin, "silu", 0.0, x, res), f"pad {pad} offset {offset}")
+    untouched()
+
+
+@pytest.mark.parametrize("rows", ["token", "slot", "sorted"])
+@pytest.mark.parametrize("T,E,k,K,N,gated", [(6000, 4, 2, 520, 2048, False), (6000, 4, 2, 512, 1000, True),
+                                             (9000, 16, 2, 264, 1024, True), (5000, 3, 1, 2048, 2048, False)])
+def test_grouped_large_tiles(T, E, k, K, N, gated, rows):
+    rng = np.random.default_rng(T)
+    idx = routing(rng, T, E, k, 0.7)
+    idx[rng.random(idx.shape) < 0.02] = E
+    for act, od, clamp in (("silu", BF16, 0.0), ("gelu", F32, 0.9)):
+        log(f"[case] grouped large T={T} E={E} K={K} N={N} gated={gated} rows={rows} {act}")
+        check_grouped(idx, E, K, N, BF16, gated, True, act, od, rows, clamp=clamp, tag=name(T=T, E=E, rows=rows, act=act))
+
+
+def test_offsets_past_32_bits():
+    """Rows of x and out spread over more than 4 GiB, in order and gathered through a plan."""
+    g = gen(13)
+    T, K, N, stride = 140000, 64, 40, 16384  # 32 KiB between rows: 4.6 GB
+    xb = torch.empty((T, stride), dtype=BF16, device="cuda")
+    x = xb[:, :K]
+    x.copy_(normal(g, (T, K), BF16))
+    ob = torch.empty((T, stride), dtype=BF16, device="cuda")
+    out = ob[:, :N]
+    lin = make_linear(g, None, N, K, BF16, False, True, "none", BF16)
+    moe.matmul(lin, x, out=out)
+    torch.cuda.synchronize()
+    ref.check(out, *reference(lin, "none", 0.0, x), "in order")
+    el = make_linear(g, 2, N, K, BF16, False, False, "none", BF16)
+    idx = (torch.arange(T, device="cuda") * 7 // 3 % 2).to(torch.int32).view(T, 1)
+    plan = moe.expert_plan(idx, 2)
+    for rows in ("token", "sorted"):
+        out.zero_()
+        moe.grouped_matmul(el, x, plan, T, top_k=1, rows=rows, out=out)
+        torch.cuda.synchronize()
+        for e in range(2):
+            if rows == "token":
+                mine = torch.nonzero(idx[:, 0] == e)[:, 0]
+            else:
+                c = int((idx == 0).sum())
+                mine = torch.arange(c, device="cuda") if e == 0 else torch.arange(c, T, device="cuda")
+            ref.check(out[mine], *ref.product(x[mine], el.w[e], out_dtype=BF16), f"{rows} e={e}")
+
+
 def test_matmul_of_no_rows():
     lin = make_linear(gen(1), None, 8, 8, BF16, False, False, "none", BF16)
     assert moe.matmul(lin, torch.empty((0, 8), dtype=BF16, device="cuda")).shape == (0, 8)
