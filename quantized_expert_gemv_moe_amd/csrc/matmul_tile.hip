@@ -35,26 +35,46 @@
 
 namespace moe {
 
-// One 64-byte step with the accumulator held in accumulation registers: a wave's 64
-// accumulators fill all 256 of them, and the compiler, left to choose, mixes
-// the two register files and moves operands between them (two moves for every
-// product, and spills).  The compiler knows nothing of
-// the waits that matrix instructions need, so what reads an accumulator next goes through
-// settle() first, and so does what is written before the first step.
-template <int DT>
+// One 64-byte step of an accumulator that stays in its registers: accumulation registers
+// (V false) or ordinary ones.  A wave's 64 accumulators fill 256 registers, and the compiler,
+// left to choose, mixes the two files and moves operands between them (two moves for
+// every product, and spills).  The last row of eight stands in ordinary registers, so
+// that neither file is full: with all 256 accumulation registers taken the compiler
+// has no room to place them and moves them about after all.  It knows nothing of the
+// waits that matrix instructions need, so what reads an accumulator next goes
+// through settle() first, and so does what is written before the first step.
+template <int DT, bool V>
 __device__ __forceinline__ void mma_acc(const mm_u32x4 &a, const mm_u32x4 &b, mm_f32x4 &c) {
-    if constexpr (DT == MOE_DTYPE_BF16)
-        asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
-    else
-        asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    if constexpr (DT == MOE_DTYPE_BF16) {
+        if constexpr (V)
+            asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+        else
+            asm("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    } else {
+        if constexpr (V)
+            asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+v"(c) : "v"(a), "v"(b));
+        else
+            asm("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    }
+}
+// Holds N accumulators in their registers up to here; without it the compiler copies
+// all of them out before it branches over the forms of the output, and spills.
+template <int N, bool V>
+__device__ __forceinline__ void hold(mm_f32x4 *c) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        if constexpr (V)
+            asm volatile("" : "+v"(c[n]));
+        else
+            asm volatile("" : "+a"(c[n]));
+    }
 }
 template <int MT, int NT>
 __device__ __forceinline__ void settle(mm_f32x4 (*c)[NT]) {
     asm volatile("s_nop 15\n\ts_nop 15");
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) asm volatile("" : "+a"(c[m][n]));
+    for (int m = 0; m < MT - 1; ++m) hold<NT, false>(c[m]);
+    hold<NT, true>(c[MT - 1]);
 }
 
 template <int DT, bool GATED, int MT, int NT>
@@ -110,39 +130,32 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
         }
     }
     const int chunks = (a.K * kElemBytes<DT>) >> 4;  // of a row
-    const int full = chunks >> 3, steps = (chunks + 7) >> 3;
+    // an odd last step is followed by one of zeros
+    const int full = chunks >> 3, steps = (chunks + 15) / 16 * 2;
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
 
-    auto load_x = [&](int h, int s, auto whole, auto part) {
-        const uint32_t at = lds0 + (s & 1) * STAGE + h * XH + wave * XI * 1024;
-        if (whole || s < full) {
-            const char *b = xbase + (int64_t)s * 128;
+    // Part of the loads of half tile h of step s: whole steps, or the last one of a row that
+    // ends inside it, with zeros past the end.
+    auto chunk_of = [&](int p) { return (lane & 7) ^ ((p >> 1) & 7); };
+    auto load = [&](uint32_t at, const char *base, const uint32_t *off, int first, int last, int row, int s, bool whole)
+        __attribute__((always_inline)) {
+        const char *b = base + (int64_t)s * 128;
 #pragma unroll
-            for (int i = from(part, XI); i < upto(part, XI); ++i) dma16(at + i * 1024, b, xo[h][i]);
-        } else if (s < steps) {  // the last, partial step: zeros past the row's end
-#pragma unroll
-            for (int i = from(part, XI); i < upto(part, XI); ++i) {
-                const int p = (wave * XI + i) * 8 + (lane >> 3);
-                const int c = (lane & 7) ^ ((p >> 1) & 7);
-                dma16(at + i * 1024, s * 8 + c < chunks ? xbase + (int64_t)s * 128 + xo[h][i] : (const char *)&kZeroChunk);
-            }
+        for (int i = first; i < last; ++i) {
+            if (whole)
+                dma16(at + i * 1024, b, off[i]);
+            else
+                dma16(at + i * 1024, s * 8 + chunk_of((row + i) * 8 + (lane >> 3)) < chunks ? b + off[i]
+                                                                                         : (const char *)&kZeroChunk);
         }
     };
-    auto load_w = [&](int h, int s, auto whole, auto part) {
-        const uint32_t at = lds0 + (s & 1) * STAGE + 2 * XH + h * WH + wave * WI * 1024;
-        const char *base = h ? ubase : wbase;
-        if (whole || s < full) {
-            const char *b = base + (int64_t)s * 128;
-#pragma unroll
-            for (int i = from(part, WI); i < upto(part, WI); ++i) dma16(at + i * 1024, b, wo[h][i]);
-        } else if (s < steps) {
-#pragma unroll
-            for (int i = from(part, WI); i < upto(part, WI); ++i) {
-                const int p = (wave * WI + i) * 8 + (lane >> 3);
-                const int c = (lane & 7) ^ ((p >> 1) & 7);
-                dma16(at + i * 1024, s * 8 + c < chunks ? base + (int64_t)s * 128 + wo[h][i] : (const char *)&kZeroChunk);
-            }
-        }
+    auto load_x = [&](int h, int s, bool whole, auto part) __attribute__((always_inline)) {
+        load(lds0 + (s & 1) * STAGE + h * XH + wave * XI * 1024, xbase, xo[h], from(part, XI), upto(part, XI),
+             wave * XI, s, whole);
+    };
+    auto load_w = [&](int h, int s, bool whole, auto part) __attribute__((always_inline)) {
+        load(lds0 + (s & 1) * STAGE + 2 * XH + h * WH + wave * WI * 1024, h ? ubase : wbase, wo[h], from(part, WI),
+             upto(part, WI), wave * WI, s, whole);
     };
 
     mm_f32x4 acc[MT][NT];
@@ -153,54 +166,48 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
     if constexpr (ACC) settle<MT, NT>(acc);
     mm_u32x4 x0[MT / 2][2], x1[MT / 2][2], wa[NT / 2][2], wb[NT / 2][2];
     const int sw = (r16 >> 1) & 7;
-    auto read_x = [&](mm_u32x4(*f)[2], int h, int s, auto part) {
+    auto read_x = [&](mm_u32x4(*f)[2], int h, int s, auto part) __attribute__((always_inline)) {
         const char *at = lds + (s & 1) * STAGE + h * XH + (wm * 8 * MT + r16) * 128;
 #pragma unroll
         for (int i = from(part, MT); i < upto(part, MT); ++i)
             f[i / 2][i % 2] = *(const mm_u32x4 *)(at + i / 2 * 2048 + (((4 * (i % 2) + g) ^ sw) << 4));
     };
-    auto read_w = [&](mm_u32x4(*f)[2], int h, int s, auto part) {
+    auto read_w = [&](mm_u32x4(*f)[2], int h, int s, auto part) __attribute__((always_inline)) {
         const char *at = lds + (s & 1) * STAGE + 2 * XH + h * WH + (wn * 8 * NT + r16) * 128;
 #pragma unroll
         for (int i = from(part, NT); i < upto(part, NT); ++i)
             f[i / 2][i % 2] = *(const mm_u32x4 *)(at + i / 2 * 2048 + (((4 * (i % 2) + g) ^ sw) << 4));
     };
-    auto multiply = [&](const mm_u32x4(*xf)[2], const mm_u32x4(*wf)[2], int mh, int nh, auto part) {
-        constexpr int PER = (MT / 2) * (NT / 2);
-#pragma unroll
-        for (int i = from(part, 2 * PER); i < upto(part, 2 * PER); ++i) {
-            const int k = i / PER, m = i % PER / (NT / 2), n = i % (NT / 2);
+    auto multiply = [&](const mm_u32x4(*xf)[2], const mm_u32x4(*wf)[2], auto mh, auto nh, auto part) __attribute__((always_inline)) {
+        constexpr int PER = (MT / 2) * (NT / 2), FROM = from(decltype(part){}, 2 * PER);
+        static_for<upto(decltype(part){}, 2 * PER) - FROM>([&](auto q) __attribute__((always_inline)) {
+            constexpr int i = FROM + q, k = i / PER, m = i % PER / (NT / 2), n = i % (NT / 2);
             mm_f32x4 &c = acc[mh * (MT / 2) + m][nh * (NT / 2) + n];
             if constexpr (ACC)
-                mma_acc<DT>(wf[n][k], xf[m][k], c);
+                mma_acc<DT, mh * (MT / 2) + m == MT - 1>(wf[n][k], xf[m][k], c);
             else
                 c = mma<DT>(wf[n][k], xf[m][k], c);
-        }
+        });
     };
 
-    // two steps' half tiles in the order of their use, then X0 and W0 of the first
-    // into registers
+    // two steps' half tiles in the order of their use, then X0 of the first into registers
     constexpr Part<0, 1> all;
     for (int i = 0; i < 2; ++i) {
-        load_x(0, i, No{}, all);
-        load_w(0, i, No{}, all);
-        load_x(1, i, No{}, all);
-        load_w(1, i, No{}, all);
+        load_x(0, i, i < full, all);
+        load_w(0, i, i < full, all);
+        load_x(1, i, i < full, all);
+        load_w(1, i, i < full, all);
     }
-    if (steps > 1)
-        wait_loads<3 * XI + 3 * WI>();
-    else
-        wait_loads<0>();
+    wait_loads<3 * XI + 3 * WI>();
     meet();
     read_x(x0, 0, 0, all);
-    read_w(wa, 0, 0, all);
 
     // A quadrant: its products in sixteen parts, after each of them one LDS read or load
     // into LDS, kept in this order: a few instructions fit beside every matrix
     // instruction, more in a row would leave the matrix core idle.  The last parts have
     // no reads, so that they have arrived when the next barrier waits for them.
-    auto quadrant = [&](auto &&load, auto &&read, auto &&mul) {
-        static_for<16>([&](auto i) {
+    auto quadrant = [&](auto &&load, auto &&read, auto &&mul) __attribute__((always_inline)) {
+        static_for<16>([&](auto i) __attribute__((always_inline)) {
             constexpr int I = decltype(i)::value;
             constexpr int R = I - (I + 2) / 4;  // parts before this one without a load
             mul(Part<I, 16>{});
@@ -211,33 +218,48 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    // `whole`: steps s+1 and s+2 are there and whole.  Towards the end the waits are
-    // for everything, since fewer loads follow than the counts assume.
-    auto step = [&](int s, mm_u32x4(*w0)[2], mm_u32x4(*w1)[2], auto whole) {
-        const bool next = whole || s + 1 < steps;
-        whole ? wait_loads<2 * XI + 2 * WI>() : wait_loads<0>();
+    // Step s, W0 in w0.  kLoad: step s + 2 follows and is whole; kEnd: it follows and may
+    // end inside or be zeros; kNext: only step s + 1 follows; kLast: none does.  No branches inside:
+    // they cost more than the products, and the compiler moves accumulators at them.
+    enum Kind { kLoad, kEnd, kNext, kLast };
+    auto step = [&](int s, mm_u32x4(*w0)[2], mm_u32x4(*w1)[2], auto kind) __attribute__((always_inline)) {
+        constexpr int K = decltype(kind)::value;
+        constexpr bool loads = K == kLoad || K == kEnd, next = K != kLast;
+        if constexpr (next)
+            wait_loads<2 * XI + 2 * WI>();
+        else
+            wait_loads<0>();
         meet();
-        quadrant([&](auto p) { load_x(0, s + 2, whole, p); }, [&](auto p) { read_w(w1, 1, s, p); },
-                 [&](auto p) { multiply(x0, w0, 0, 0, p); });
-        quadrant([&](auto p) { load_w(0, s + 2, whole, p); }, [&](auto p) { read_x(x1, 1, s, p); },
-                 [&](auto p) { multiply(x0, w1, 0, 1, p); });
-        whole ? wait_loads<2 * XI + 2 * WI>() : wait_loads<0>();
-        meet();
-        quadrant([&](auto p) { load_x(1, s + 2, whole, p); }, [&](auto p) { if (next) read_x(x0, 0, s + 1, p); },
-                 [&](auto p) { multiply(x1, w1, 1, 1, p); });
-        quadrant([&](auto p) { load_w(1, s + 2, whole, p); }, [&](auto p) { if (next) read_w(w1, 0, s + 1, p); },
-                 [&](auto p) { multiply(x1, w0, 1, 0, p); });
+        quadrant([&](auto p) __attribute__((always_inline)) { if constexpr (loads) load_x(0, s + 2, K == kLoad, p); },
+                 [&](auto p) __attribute__((always_inline)) { read_w(w1, 1, s, p); },
+                 [&](auto p) __attribute__((always_inline)) { multiply(x0, w0, Index<0>{}, Index<0>{}, p); });
+        quadrant([&](auto p) __attribute__((always_inline)) { if constexpr (loads) load_w(0, s + 2, K == kLoad, p); },
+                 [&](auto p) __attribute__((always_inline)) { read_x(x1, 1, s, p); },
+                 [&](auto p) __attribute__((always_inline)) { multiply(x0, w1, Index<0>{}, Index<1>{}, p); });
+        if constexpr (next) {
+            wait_loads<(loads ? 2 : 1) * (XI + WI)>();
+            meet();
+        }
+        quadrant([&](auto p) __attribute__((always_inline)) { if constexpr (loads) load_x(1, s + 2, K == kLoad, p); },
+                 [&](auto p) __attribute__((always_inline)) { if constexpr (next) read_x(x0, 0, s + 1, p); },
+                 [&](auto p) __attribute__((always_inline)) { multiply(x1, w1, Index<1>{}, Index<1>{}, p); });
+        quadrant([&](auto p) __attribute__((always_inline)) { if constexpr (loads) load_w(1, s + 2, K == kLoad, p); },
+                 [&](auto p) __attribute__((always_inline)) { if constexpr (next) read_w(w1, 0, s + 1, p); },
+                 [&](auto p) __attribute__((always_inline)) { multiply(x1, w0, Index<1>{}, Index<0>{}, p); });
     };
+    // W0 changes registers every step, so steps go by pairs, all of them in one line.
+    read_w(wa, 0, 0, all);
     int s = 0;
     for (; s + 3 < full; s += 2) {
-        step(s, wa, wb, Yes{});
-        step(s + 1, wb, wa, Yes{});
+        step(s, wa, wb, Index<kLoad>{});
+        step(s + 1, wb, wa, Index<kLoad>{});
     }
-    for (; s < steps; s += 2) {
-        step(s, wa, wb, No{});
-        if (s + 1 < steps) step(s + 1, wb, wa, No{});
+    for (; s + 2 < steps; s += 2) {
+        step(s, wa, wb, Index<kEnd>{});
+        step(s + 1, wb, wa, Index<kEnd>{});
     }
-
+    step(s, wa, wb, Index<kNext>{});
+    step(s + 1, wb, wa, Index<kLast>{});
     if constexpr (ACC) settle<MT, NT>(acc);
     // The results.  Code that runs once a tile comes out of the caches slowly, and
     // branches over the forms not taken made up a third of a tile's fixed 23 us;
@@ -265,6 +287,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
                     __builtin_amdgcn_sched_barrier(0);  // all rows together would not fit the registers
                     if constexpr (m + 1 < MT) fetch(Index<m + 1>{});
                     mm_f32x4 *z = acc[m];
+                    if constexpr (ACC) hold<NT, m == MT - 1>(z);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) z[n] += b[n];
                     if (a.clamp > 0.f) {
@@ -312,8 +335,11 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
     mm_f32x4 *mine = (mm_f32x4 *)lds + wave * (PASS * NT * 64) + lane;
     __syncthreads();  // every wave has read its operands
     static_for<MT / PASS>([&](auto pass) __attribute__((always_inline)) {
-        static_for<PASS * NT>([&](auto i) __attribute__((always_inline)) {
-            mine[i * 64] = acc[pass * PASS + i / NT][i % NT];
+        static_for<PASS>([&](auto m) __attribute__((always_inline)) {
+            mm_f32x4 *z = acc[pass * PASS + m];
+            if constexpr (ACC) hold<NT, pass * PASS + m == MT - 1>(z);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mine[(m * NT + n) * 64] = z[n];
         });
 #pragma unroll 1
         for (int i = 0; i < PASS * NTC; ++i) {
