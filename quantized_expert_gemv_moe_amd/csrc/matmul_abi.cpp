@@ -71,20 +71,25 @@ static int64_t ragged_tiles(int64_t rows, int64_t groups, int64_t tile) {
 }
 
 // Microseconds that a kernel takes, roughly: `fixed` for a launch, then for every
-// 256 tiles (a tile on each CU) `round` and `step` for each 128 bytes of a row, at
-// least `alone` a step when the tiles are fewer.  Fitted to measurements of
-// every kernel on one another's shapes (dense: 1 to 4096 rows, K 768 to 8192, N 512 to 4096; grouped: 1 to
-// 4096 tokens, 128 experts, top-8, K 768 and 2048), where the choice made with it
-// is within 10 % of the best kernel.  What separates them: below some 64 rows
-// splitting K over a workgroup's waves wins (2048 x 2048 bf16, 16 rows: 6.2 us
-// against 8.8 of the 64 x 64 tile), then the tile grows with the work (1024 rows:
-// 64 x 128 13.8, 64 x 64 16.1, 128 x 128 24.1 us; 4096 rows: 128 x 128 37.1, 64 x
-// 128 43.1, 256 x 256 60.4 us; 8192 rows of K 8192, N 4096: 256 x 256 432 us, 128 x
-// 128 507 us; 128 experts, top-8, 768 -> 2048: 16 tokens 32 x 64 42.6, 64 x 64 49.3
-// us, 512 tokens 32 x 64 99.6, 64 x 128 93.5 us).  fp32 steps take some three times as long: the matrix cores'
-// rate.  Rows at odd addresses cost the kernel for few rows 2.3 times as much (16
-// rows, K 4096 and 4099, N 512: 9.5 and 19.5 us), so the register tile takes over
-// earlier (512 rows of 2047 by 2048: 16.5 us).
+// 256 tiles (a tile on each CU) `round`, more or less of it with the bytes of a tile's
+// results, and `step` for each 128 bytes of a row, `alone` a step when the tiles are fewer.
+// Fitted to measurements of every kernel on one another's shapes (dense: 1 to 16384
+// rows, K 256 to 8192, N 512 to 4096; grouped: 1 to 16384 tokens, 128 experts, top-8,
+// K 768 and 2048), where the choice made with it is mostly within 5 %, at worst some 15
+// %, of the best kernel.  What separates them (bf16, us):
+//   16 rows, 2048 -> 2048      K over the waves 6.2, 64 x 64 tile 8.8
+//   1024 rows, 2048 -> 2048    64 x 128 13.8, 64 x 64 16.1, 128 x 128 17.9, 256 x 256 37
+//   4096 rows, 2048 -> 2048    128 x 128 33.4, 64 x 128 and 256 x 256 43.4
+//   4096 rows, 4096 -> 4096    256 x 256 92.5 (1.49 PFLOP/s), 128 x 128 117
+//   4096 rows, 256 -> 4096     128 x 128 16.4, 256 x 256 17.1, 64 x 128 22.7
+//   16 tokens, 768 -> 2048     32 x 64 42.6, 64 x 64 49.3
+//   512 tokens, 768 -> 2048    64 x 128 93.5, 32 x 64 99.6
+//   1024 tokens, 2048 -> 768   gated: 128 x 128 152, 64 x 128 175, 256 x 256 174
+//   16384 tokens, 2048 -> 768  gated: 256 x 256 719, 128 x 128 897
+// fp32 steps take some three times as long: the matrix cores' rate.  Rows at odd
+// addresses cost the kernel for few rows 2.3 times as much (16 rows, K 4096 and 4099, N
+// 512: 9.5 and 19.5 us), so the register tile takes over earlier (512 rows of 2047 by
+// 2048: 16.5 us).
 struct Cost {
     MatmulKernel kernel;
     int mt, nt;
@@ -93,7 +98,7 @@ struct Cost {
 static const Cost kCosts[] = {
     {kMatmulDeep, 1, 2, 3.3, 0.2, 0.13, 0.19},
     {kMatmulDeep, 2, 2, 3.3, 0.3, 0.20, 0.19}, {kMatmulDeep, 2, 4, 3.3, 0.5, 0.37, 0.27},
-    {kMatmulTile, 4, 4, 3.3, 1.2, 0.45, 0.54}, {kMatmulTile, 8, 8, 3.3, 3.0, 1.55, 1.10},
+    {kMatmulTile, 4, 4, 3.3, 1.3, 0.48, 0.54}, {kMatmulTile, 8, 8, 3.3, 8.5, 1.31, 0.92},
     {kMatmulAny, 2, 2, 3.3, 0.5, 0.36, 0.40},  {kMatmulFew, 1, 0, 2.7, 0.0, 0.116, 0.116},
     {kMatmulFew, 2, 0, 2.7, 0.0, 0.170, 0.170}};
 
@@ -128,10 +133,14 @@ MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bo
         const double rounds = n <= 256 ? 1 : (double)(int64_t)((n + 255) / 256);
         double step = n <= 256 && k.alone > k.step ? k.alone : n <= 128 ? k.alone : k.step * rounds;
         if (f32 && !few) step *= 3;
+        // experts that fill less than half of the largest tile (256 experts of 96 rows, 4096
+        // -> 2048 gated: 256 x 256 1836, 128 x 128 1670 us; 128 of 128 rows: 183 and 207 us)
+        if (grouped && k.mt == 8 && rows < 128 * used) step *= 1.15;
         if (few && gated && k.mt == 2) step *= 1.4;
         if (few && !is_aligned) step *= 2.3;
         if (few && rows <= 4) step *= 0.75;  // x is one line for all lanes of a step
-        const double time = k.fixed + k.round * rounds + step * steps;
+        const double round = k.round * (0.5 + 0.25 * dtype_size(L->out_dtype) * (gated ? 0.5 : 1.0));
+        const double time = k.fixed + round * rounds + step * steps;
         auto take = [&](double t, int splits) {
             if (best.tiles_n && t >= best_time) return;
             best_time = t;
@@ -148,7 +157,7 @@ MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bo
         // K in stretches: a second launch and a pass over the parts, so it has to gain
         // more than those cost
         for (int splits = 2; splits <= kMaxSplits && tm * tn * splits <= kMaxSplitTiles && splits * 4 <= steps; splits *= 2)
-            take(k.fixed + k.round + k.alone * (f32 ? 3 : 1) * (tm * tn * splits > 128 ? 2 : 1) * steps / splits + kJoinCost,
+            take(k.fixed + round + k.alone * (f32 ? 3 : 1) * (tm * tn * splits > 128 ? 2 : 1) * steps / splits + kJoinCost,
                  splits);
     }
     return best;  // tiles_n == 0: more workgroups than a launch takes

@@ -21,12 +21,12 @@
 // the global side: lane l of a load fetches chunk (l % 8) ^ ((row / 2) % 8) of its row.
 // Counters: no bank conflicts.
 //
-// What bounds it: at 8192 x 8192 x 4096 bf16 the matrix cores are busy 62 % of the time
-// at 1.8 GHz, the clock that the power limit leaves (1.35 PFLOP/s; a library product
-// of that size, without bias and residual, 1.42 to 1.48).  Copies of the loop without the
-// loads, or without the LDS reads, took 12 % less each.  A persistent form of
-// this kernel, the next tile's first loads issued before the results of the last,
-// was 9 % slower: its lookups and offsets spill, and the loads delay the results.
+// What bounds it: at 4096 x 4096 x 4096 bf16 it takes 92.5 us, 1.49 PFLOP/s, and 1.41 at
+// 8192 x 8192 x 4096 with bias and residual, where a library product without them
+// reaches 1.42 to 1.48: the power limit's clock (1.8 GHz under this load) and the
+// issue of loads and LDS reads beside the matrix instructions (copies of the loop
+// without the one or the other took 12 % less each).  A tile's start and end cost 9 us
+// a round beside the steps, 7 of them the bytes of 256 tiles' results.
 #include <hip/hip_runtime.h>
 
 #include "matmul_device.h"
