@@ -557,7 +557,7 @@ class Linear:
     struct: LinearStruct
 
     def __post_init__(self):
-        self.dtype, self.device = self.w.dtype, self.w.device
+        self.dtype, self.device, self.index = self.w.dtype, self.w.device, self.w.get_device()
         self._ref = C.byref(self.struct)
 
     @staticmethod
@@ -680,27 +680,26 @@ def matmul(linear: Linear, x: torch.Tensor, residual: Optional[torch.Tensor] = N
     """moe_matmul: x [rows, in] -> out [rows, out] = residual + f(x w^T + bias), f gated when the
     linear has w_up.  Rows of x, residual and out may be strided; residual is any of the three
     types; out may be residual itself."""
-    device = linear.device
-    if stream is not None or _get_device() != device.index:
-        return _on(device, stream, lambda handle: _matmul(linear, x, residual, out, workspace, handle))
-    return _matmul(linear, x, residual, out, workspace, _raw_stream(device.index))
+    if stream is not None or _get_device() != linear.index:
+        return _on(linear.device, stream, lambda handle: _matmul(linear, x, residual, out, workspace, handle))
+    return _matmul(linear, x, residual, out, workspace, _raw_stream(linear.index))
 
 
 def _matmul(linear, x, residual, out, workspace, handle):
-    device, K, N = linear.device, linear.in_features, linear.out_features
-    if x.dim() != 2 or x.shape[1] != K or x.dtype is not linear.dtype or x.device != device:
+    device, index, K, N = linear.device, linear.index, linear.in_features, linear.out_features
+    if x.dim() != 2 or x.shape[1] != K or x.dtype is not linear.dtype or x.get_device() != index:
         _refuse("x", x, "rows", K, linear.dtype, device)
     rows = x.shape[0]
     res = None
     res_type = res_stride = 0
     if residual is not None:
         res_type = _DTYPES.get(residual.dtype)
-        if residual.shape != (rows, N) or residual.device != device or res_type is None:
+        if residual.shape != (rows, N) or residual.get_device() != index or res_type is None:
             _refuse("residual", residual, rows, N, "bf16, fp16 or fp32", device)
         res, res_stride = residual.data_ptr(), _strides(residual, rows, N, "residual")
     if out is None:
         out = torch.empty((rows, N), dtype=linear.out_dtype, device=device)
-    elif out.shape != (rows, N) or out.dtype is not linear.out_dtype or out.device != device:
+    elif out.shape != (rows, N) or out.dtype is not linear.out_dtype or out.get_device() != index:
         _refuse("out", out, rows, N, linear.out_dtype, device)
     L = lib()
     ws = _workspace(workspace, L.moe_matmul_workspace_size, linear, rows)
@@ -719,33 +718,33 @@ def grouped_matmul(linear: Linear, x: torch.Tensor, plan: Plan, n_slots: int, to
     row per token, slot s reads row s // top_k), "slot" (x has a row per slot) or "sorted"
     (rows of x and out lie grouped by expert, in the plan's order).  Rows of slots that the
     plan does not list are left as they are (unset when out is allocated here)."""
-    device, n_slots, top_k = linear.device, int(n_slots), int(top_k)
-    if stream is not None or _get_device() != device.index:
-        return _on(device, stream,
+    n_slots, top_k = int(n_slots), int(top_k)
+    if stream is not None or _get_device() != linear.index:
+        return _on(linear.device, stream,
                    lambda handle: _grouped(linear, x, plan, n_slots, top_k, rows, out, workspace, handle))
-    return _grouped(linear, x, plan, n_slots, top_k, rows, out, workspace, _raw_stream(device.index))
+    return _grouped(linear, x, plan, n_slots, top_k, rows, out, workspace, _raw_stream(linear.index))
 
 
 def _grouped(linear, x, plan, n_slots, top_k, rows, out, workspace, handle):
-    device, K, N = linear.device, linear.in_features, linear.out_features
+    device, index, K, N = linear.device, linear.index, linear.in_features, linear.out_features
     mode = _ROWS.get(rows)
     if mode is None:
         raise ValueError(f"rows must be one of {sorted(_ROWS)}")
     if n_slots < 0 or top_k < 1:
         raise ValueError("n_slots must be at least 0 and top_k at least 1")
-    if x.dim() != 2 or x.shape[1] != K or x.dtype is not linear.dtype or x.device != device:
+    if x.dim() != 2 or x.shape[1] != K or x.dtype is not linear.dtype or x.get_device() != index:
         _refuse("x", x, "rows", K, linear.dtype, device)
     x_rows = x.shape[0]
     if x_rows != (-(-n_slots // top_k) if mode == MOE_ROWS_TOKEN else n_slots):
         raise ValueError(f"x has {x_rows} rows, which does not fit {n_slots} slots with rows={rows!r}, top_k={top_k}")
     work, slots = plan.work, plan.sorted_slots
-    if work.numel() < 4 * min(linear.n_groups, max(n_slots, 1)) or work.device != device:
+    if work.numel() < 4 * min(linear.n_groups, max(n_slots, 1)) or work.get_device() != index:
         raise ValueError(f"the plan's records are too few for {linear.n_groups} experts or not on {device}")
-    if mode != MOE_ROWS_SORTED and (slots.numel() < n_slots or slots.device != device):
+    if mode != MOE_ROWS_SORTED and (slots.numel() < n_slots or slots.get_device() != index):
         raise ValueError(f"the plan's sorted_slots are fewer than {n_slots} or not on {device}")
     if out is None:
         out = torch.empty((n_slots, N), dtype=linear.out_dtype, device=device)
-    elif out.shape != (n_slots, N) or out.dtype is not linear.out_dtype or out.device != device:
+    elif out.shape != (n_slots, N) or out.dtype is not linear.out_dtype or out.get_device() != index:
         _refuse("out", out, n_slots, N, linear.out_dtype, device)
     L = lib()
     ws = _workspace(workspace, L.moe_grouped_workspace_size, linear, n_slots)
@@ -764,30 +763,30 @@ def combine(y: torch.Tensor, idx: torch.Tensor, w: torch.Tensor, n_experts: int,
     """moe_combine: y [B * k, H], idx int32 [B, k], w fp32 [B, k] -> out [B, H] =
     residual + the weighted sum of each token's k rows.  out_dtype defaults to out's type, else
     the residual's, else y's."""
-    device = y.device
-    if not y.is_cuda:
+    index = y.get_device()
+    if index < 0:
         raise ValueError("y must be a contiguous bf16, fp16 or fp32 [slots, hidden] device tensor")
-    if stream is not None or _get_device() != device.index:
-        return _on(device, stream, lambda handle: _combine(y, idx, w, n_experts, residual, out, out_dtype, handle))
-    return _combine(y, idx, w, n_experts, residual, out, out_dtype, _raw_stream(device.index))
+    if stream is not None or _get_device() != index:
+        return _on(y.device, stream, lambda handle: _combine(y, idx, w, n_experts, residual, out, out_dtype, handle))
+    return _combine(y, idx, w, n_experts, residual, out, out_dtype, _raw_stream(index))
 
 
 def _combine(y, idx, w, n_experts, residual, out, out_dtype, handle):
-    device, y_type = y.device, _DTYPES.get(y.dtype)
+    device, index, y_type = y.device, y.get_device(), _DTYPES.get(y.dtype)
     if y.dim() != 2 or y_type is None or not y.is_contiguous():
         raise ValueError("y must be a contiguous bf16, fp16 or fp32 [slots, hidden] device tensor")
     H = y.shape[1]
-    if idx.dim() != 2 or idx.dtype is not torch.int32 or not idx.is_contiguous() or idx.device != device:
+    if idx.dim() != 2 or idx.dtype is not torch.int32 or not idx.is_contiguous() or idx.get_device() != index:
         raise ValueError(f"idx must be a contiguous int32 [B, k] tensor on {device}")
     B, k = idx.shape
-    if w.dtype is not torch.float32 or w.shape != idx.shape or not w.is_contiguous() or w.device != device:
+    if w.dtype is not torch.float32 or w.shape != idx.shape or not w.is_contiguous() or w.get_device() != index:
         _refuse("w", w, B, k, "contiguous fp32", device)
     if y.shape[0] != B * k:
         raise ValueError(f"y has {y.shape[0]} rows, {B * k} needed for {B} tokens of {k} slots")
     res, res_type = None, 0
     if residual is not None:
         res_type = _DTYPES.get(residual.dtype)
-        if residual.shape != (B, H) or residual.device != device or res_type is None or not residual.is_contiguous():
+        if residual.shape != (B, H) or residual.get_device() != index or res_type is None or not residual.is_contiguous():
             _refuse("residual", residual, B, H, "contiguous bf16, fp16 or fp32", device)
         res = residual.data_ptr()
     if out is None:
@@ -795,7 +794,7 @@ def _combine(y, idx, w, n_experts, residual, out, out_dtype, handle):
             out_dtype = y.dtype if residual is None else residual.dtype
         out = torch.empty((B, H), dtype=out_dtype, device=device)
     out_type = _DTYPES.get(out.dtype)
-    if (out.shape != (B, H) or out.device != device or out_type is None or not out.is_contiguous()
+    if (out.shape != (B, H) or out.get_device() != index or out_type is None or not out.is_contiguous()
             or (out_dtype is not None and out.dtype is not out_dtype)):
         _refuse("out", out, B, H, f"contiguous {out_dtype or 'bf16, fp16 or fp32'}", device)
     st = lib().moe_combine(y.data_ptr(), y_type, idx.data_ptr(), w.data_ptr(), B, H, k, int(n_experts), res, res_type,
