@@ -221,13 +221,12 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
                             bias_group * (int64_t)es}};
     for (const Span &s : reads)
         if (spans_overlap(so, s)) return MOE_ERR_INVALID_ARG;
-    if (grouped) {
-        const int64_t records = rows < L->n_groups ? rows : L->n_groups;
-        const Span plan_reads[2] = {{plan->work, 1, records * 16, 1},
-                                    {plan->sorted_slots, rows_mode != MOE_ROWS_SORTED, (int64_t)rows * 4, 1}};
-        for (const Span &s : plan_reads)
-            if (spans_overlap(so, s)) return MOE_ERR_INVALID_ARG;
-    }
+    const int64_t records = rows < L->n_groups ? rows : L->n_groups;
+    const Span plan_reads[2] = {{grouped ? plan->work : nullptr, grouped, records * 16, 1},
+                                {grouped ? plan->sorted_slots : nullptr, grouped && rows_mode != MOE_ROWS_SORTED,
+                                 (int64_t)rows * 4, 1}};
+    for (const Span &s : plan_reads)
+        if (spans_overlap(so, s)) return MOE_ERR_INVALID_ARG;
     const Span sr{residual, residual ? rows : 0, L->out_features * (int64_t)rs, rs_row * (int64_t)rs};
     if (spans_overlap(so, sr) && !(residual == out && residual_dtype == L->out_dtype && rs_row == os_row))
         return MOE_ERR_INVALID_ARG;
@@ -237,6 +236,8 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
         const Span sw{workspace, 1, (int64_t)choice->workspace, (int64_t)choice->workspace};
         if (spans_overlap(sw, so) || spans_overlap(sw, sr)) return MOE_ERR_INVALID_ARG;
         for (const Span &s : reads)
+            if (spans_overlap(sw, s)) return MOE_ERR_INVALID_ARG;
+        for (const Span &s : plan_reads)
             if (spans_overlap(sw, s)) return MOE_ERR_INVALID_ARG;
     }
 

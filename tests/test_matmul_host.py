@@ -169,6 +169,15 @@ def test_grouped_refusals():
     assert gcall(slots=1 << 30) == U
 
 
+def test_workspace_must_not_overlap_the_plan():
+    lin = linear(in_features=8192, out_features=512, n_groups=1)  # K goes in stretches
+    need = moe.lib().moe_grouped_workspace_size(C.byref(lin), 16)
+    ws = FAKE + 16 * GIB
+    assert 0 < need <= 4 * GIB
+    for kw in (dict(work=ws), dict(work=ws + 1024), dict(sorted_slots=ws + 256), dict(work=ws, rows=2)):
+        assert gcall(lin=lin, slots=16, **kw) == moe.MOE_ERR_INVALID_ARG, kw
+
+
 def test_combine_refusals():
     I, U = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED
 
