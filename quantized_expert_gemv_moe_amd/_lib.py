@@ -580,6 +580,8 @@ class Linear:
             raise ValueError("bias_up goes with bias and w_up")
         N, K = w.shape[-2:]
         E = w.shape[0] if w.dim() == 3 else 1
+        if max(N, K, E) > _INT32_MAX:
+            raise ValueError("the sizes of w must fit 32 bits")
         if K > 1 and w.stride(-1) != 1:
             raise ValueError("the rows of w must be contiguous")
         if w_up is not None and (w_up.shape != w.shape or w_up.dtype != w.dtype or w_up.device != w.device
@@ -661,6 +663,10 @@ def _strides(t: torch.Tensor, rows: int, cols: int, name: str) -> int:
     return s0
 
 
+# The ABI's sizes are 32 bits wide, and ctypes would pass the low 32 of a longer one.
+_INT32_MAX = 0x7FFFFFFF
+
+
 def _refuse(name: str, t: torch.Tensor, rows, cols: int, dtype, device):
     raise ValueError(f"{name} must be a {dtype} [{rows}, {cols}] tensor on {device}, "
                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
@@ -690,6 +696,8 @@ def _matmul(linear, x, residual, out, workspace, handle):
     if x.dim() != 2 or x.shape[1] != K or x.dtype is not linear.dtype or x.get_device() != index:
         _refuse("x", x, "rows", K, linear.dtype, device)
     rows = x.shape[0]
+    if rows > _INT32_MAX:
+        raise ValueError(f"x has {rows} rows, more than fit 32 bits")
     res = None
     res_type = res_stride = 0
     if residual is not None:
@@ -730,8 +738,8 @@ def _grouped(linear, x, plan, n_slots, top_k, rows, out, workspace, handle):
     mode = _ROWS.get(rows)
     if mode is None:
         raise ValueError(f"rows must be one of {sorted(_ROWS)}")
-    if n_slots < 0 or top_k < 1:
-        raise ValueError("n_slots must be at least 0 and top_k at least 1")
+    if not 0 <= n_slots <= _INT32_MAX or not 1 <= top_k <= _INT32_MAX:
+        raise ValueError("n_slots must be at least 0 and top_k at least 1, and both fit 32 bits")
     if x.dim() != 2 or x.shape[1] != K or x.dtype is not linear.dtype or x.get_device() != index:
         _refuse("x", x, "rows", K, linear.dtype, device)
     x_rows = x.shape[0]
@@ -779,6 +787,8 @@ def _combine(y, idx, w, n_experts, residual, out, out_dtype, handle):
     if idx.dim() != 2 or idx.dtype is not torch.int32 or not idx.is_contiguous() or idx.get_device() != index:
         raise ValueError(f"idx must be a contiguous int32 [B, k] tensor on {device}")
     B, k = idx.shape
+    if max(B, k, H, n_experts) > _INT32_MAX:
+        raise ValueError("the sizes of y and idx and n_experts must fit 32 bits")
     if w.dtype is not torch.float32 or w.shape != idx.shape or not w.is_contiguous() or w.get_device() != index:
         _refuse("w", w, B, k, "contiguous fp32", device)
     if y.shape[0] != B * k:

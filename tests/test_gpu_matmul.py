@@ -724,3 +724,22 @@ def test_wrappers_refuse_what_does_not_fit():
     for y in (normal(g, (7, 16), F32), normal(g, (8, 16), F32).cpu(), normal(g, (16, 8), F32).t()):
         with pytest.raises(ValueError):
             moe.combine(y, idx, w, 4)
+
+
+def test_wrappers_refuse_sizes_past_32_bits():
+    n = 2 ** 32 + 5  # 5 in the ABI's 32 bits
+    x = torch.empty((n, 1), dtype=BF16, device="cuda")
+    g = gen(35)
+    lin = make_linear(g, None, 8, 1, BF16, False, False, "none", BF16)
+    with pytest.raises(ValueError):
+        moe.matmul(lin, x, out=torch.empty((5, 8), dtype=BF16, device="cuda"))
+    for w in (x, x.view(1, n, 1), x.view(n, 1, 1)):
+        with pytest.raises(ValueError):
+            moe.Linear.from_tensors(w)
+    del x
+    el = make_linear(g, 4, 16, 32, BF16, False, False, "none", BF16)
+    idx, plan = plan_of(np.zeros((4, 2), np.int32), 4)
+    with pytest.raises(ValueError):
+        moe.grouped_matmul(el, normal(g, (4, 32), BF16), plan, 8, top_k=2 ** 32 + 2)
+    with pytest.raises(ValueError):
+        moe.combine(normal(g, (8, 16), F32), idx, torch.ones((4, 2), device="cuda"), 2 ** 32 + 4)
