@@ -21,12 +21,12 @@
 // the global side: lane l of a load fetches chunk (l % 8) ^ ((row / 2) % 8) of its row.
 // Counters: no bank conflicts.
 //
-// What bounds it: at 4096 x 4096 x 4096 bf16 it takes 92.5 us, 1.49 PFLOP/s, and 1.41 at
-// 8192 x 8192 x 4096 with bias and residual, where a library product without them
-// reaches 1.42 to 1.48: the power limit's clock (1.8 GHz under this load) and the
-// issue of loads and LDS reads beside the matrix instructions (copies of the loop
-// without the one or the other took 12 % less each).  A tile's start and end cost 9 us
-// a round beside the steps, 7 of them the bytes of 256 tiles' results.
+// What bounds it: 4096 x 4096 x 4096 bf16 takes 92.5 us and 8192 x 8192 x 4096 with bias
+// and residual 370 us, 1.49 PFLOP/s both, where a library product without them reaches
+// 1.42 to 1.48: the power limit's clock (1.81 GHz under this load) and the issue of loads
+// and LDS reads beside the matrix instructions, which keep the matrix cores busy for
+// 78 % of the cycles.  A tile's start and end cost 9 us a round beside the steps, 7 of
+// them the bytes of 256 tiles' results.
 #include <hip/hip_runtime.h>
 
 #include "matmul_device.h"
@@ -262,9 +262,9 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
     step(s + 1, wb, wa, Index<kLast>{});
     if constexpr (ACC) settle<MT, NT>(acc);
     // The results.  Code that runs once a tile comes out of the caches slowly, and
-    // branches over the forms not taken made up a third of a tile's fixed 23 us;
-    // so the usual outputs (whole, aligned columns of the weights' 16-bit type) have a
-    // straight path for each function, everything else one compact loop.
+    // branches over the forms not taken made up a third of the 23 us that a tile
+    // took beside its steps; so the usual outputs (whole, aligned columns of the weights'
+    // 16-bit type) have a straight path for each function, everything else one compact loop.
     const int col = col0 + wn * CW + lane_col<NTC>(g);
     auto row_of = [&](int m) { return wm * 16 * MT + m * 16 + r16; };
     if constexpr (DT != MOE_DTYPE_F32) {
