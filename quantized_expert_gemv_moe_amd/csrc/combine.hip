@@ -26,7 +26,6 @@ struct CombineArgs {
     int y_dtype, res_dtype, out_dtype;
     int n_tokens, hidden, top_k, n_experts;
     int groups;  // column groups of a token
-    int vec;     // four columns are one aligned access everywhere
 };
 
 __global__ __launch_bounds__(256) void combine_rows_kernel(CombineArgs a) {
@@ -39,7 +38,7 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(CombineArgs a) {
     bool bad = false;
     auto row = [&](int j) -> mm_f32x4 {
         const int64_t at = (s0 + j) * a.hidden + c;
-        if (a.vec) return load_value4(a.y, at, a.y_dtype);
+        if (c + kCombineCols <= a.hidden) return load_value4(a.y, at, a.y_dtype);
         mm_f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -62,8 +61,8 @@ __global__ __launch_bounds__(256) void combine_rows_kernel(CombineArgs a) {
     }
     for (; j < a.top_k; ++j) add(j, row(j));
     if (bad) acc = mm_f32x4{} + __builtin_nanf("");
-    store4(a.out, (int64_t)t * a.hidden, a.out_dtype, a.residual, (int64_t)t * a.hidden, a.res_dtype, a.vec, c,
-           a.hidden, acc);
+    store4(a.out, (int64_t)t * a.hidden, a.out_dtype, a.residual, (int64_t)t * a.hidden, a.res_dtype, c, a.hidden,
+           acc);
 }
 
 }  // namespace moe
@@ -77,13 +76,9 @@ extern "C" moe_status moe_combine(const void *y, int32_t y_dtype, const int32_t 
     const moe_status st = check_combine(y, y_dtype, topk_idx, topk_w, n_tokens, hidden, top_k, n_experts, residual,
                                         residual_dtype, out, out_dtype);
     if (st != MOE_OK || n_tokens == 0) return st;
-    const uintptr_t ya = 4 * dtype_size(y_dtype), oa = 4 * dtype_size(out_dtype);
-    const uintptr_t ra = residual ? 4 * dtype_size(residual_dtype) : 1;
-    const bool vec = hidden % kCombineCols == 0 && (uintptr_t)y % ya == 0 && (uintptr_t)out % oa == 0 &&
-                     (uintptr_t)residual % ra == 0;
     const int groups = (hidden + kCombineCols - 1) / kCombineCols;
     const CombineArgs a{y, topk_idx, topk_w, residual, out, y_dtype, residual_dtype, out_dtype,
-                        n_tokens, hidden, top_k, n_experts, groups, vec};
+                        n_tokens, hidden, top_k, n_experts, groups};
     const unsigned blocks = (unsigned)(((int64_t)groups * n_tokens + 255) / 256);
     hipLaunchKernelGGL(combine_rows_kernel, dim3(blocks), dim3(256), 0, (hipStream_t)hip_stream, a);
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;

@@ -267,12 +267,10 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
     a->clamp = L->clamp_limit;
     a->res_dtype = residual ? residual_dtype : L->out_dtype;
     a->out_dtype = L->out_dtype;
-    a->vec_out = aligned(out, 4 * os) && os_row % 4 == 0 &&
-                 (!residual || (aligned(residual, 4 * rs) && rs_row % 4 == 0));
-    if (a->vec_out && aligned(out, 8 * os) && os_row % 8 == 0) a->vec_out = 2;
-    if (a->vec_out == 2 &&
+    a->vec_out = aligned(out, 8 * os) && os_row % 8 == 0;
+    if (a->vec_out &&
         (!residual || (aligned(residual, 8 * rs) && rs_row % 8 == 0 && residual_dtype == L->out_dtype)))
-        a->vec_out = 3;
+        a->vec_out = 2;
     a->n_records = rows < L->n_groups ? rows : L->n_groups;
     a->tiles_m = choice->tiles_m;
     a->tiles_n = choice->tiles_n;

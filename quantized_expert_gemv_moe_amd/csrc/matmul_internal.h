@@ -28,8 +28,8 @@ struct MatmulArgs {
     int K, N, groups, top_k, rows_mode, fn;
     float clamp;
     int res_dtype, out_dtype;
-    int vec_out;         // out and residual take vector accesses of 4 columns (1), out also of 8 (2),
-                         // and the residual, of out's type, too (3)
+    int vec_out;         // rows of out are aligned for 8 columns at a time (1), and the residual, of
+                         // out's type, too (2)
     int n_records;       // plan records that can be in use
     int tiles_m, tiles_n;
 };

@@ -268,7 +268,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a) {
     const int col = col0 + wn * CW + lane_col<NTC>(g);
     auto row_of = [&](int m) { return wm * 16 * MT + m * 16 + r16; };
     if constexpr (DT != MOE_DTYPE_F32) {
-        if (a.vec_out == 3 && a.out_dtype == DT && col0 + 2 * CW <= a.N) {
+        if (a.vec_out == 2 && a.out_dtype == DT && col0 + 2 * CW <= a.N) {
             mm_f32x4 b[NT];
             load_bias<DT, GATED, NT>(a, t.group, col, b);
             auto straight = [&](auto f, auto has_residual) __attribute__((always_inline)) {
