@@ -3,8 +3,10 @@
 //
 // They are issued as inline assembly without results, because the compiler would wait
 // for all loads in flight before any LDS read that may alias their target; the waits
-// that replace it are written out.  A wave's load puts lane l's 16 bytes at 16 l of
-// a 1 KiB block of LDS: eight rows of 128 bytes.
+// that replace it are written out.  m0 holds the target and is an operand, so that the
+// compiler, which has uses of its own for it, knows what stands there (one wait state
+// behind its write).  A wave's load puts lane l's 16 bytes at 16 l of a 1 KiB block of LDS:
+// eight rows of 128 bytes.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -18,11 +20,10 @@ static __device__ const mm_u32x4 kZeroChunk = {0u, 0u, 0u, 0u};
 
 // 16 bytes a lane, from base + off (32 bits, unsigned), to lds + 16 * lane.
 __device__ __forceinline__ void dma16(uint32_t lds, const char *base, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base)
-                 : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(lds), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void dma16(uint32_t lds, const char *from) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(lds), "v"(from) : "memory");
 }
 
 struct Yes {
