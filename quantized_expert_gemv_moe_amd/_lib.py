@@ -635,8 +635,11 @@ def alloc_grouped_workspace(linear: Linear, max_slots: int) -> Optional[torch.Te
     return _alloc_bytes(grouped_workspace_size(linear, max_slots), linear.w.device)
 
 
-_get_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The calls beneath torch.cuda's own, for the path of every call; builds of torch without a
+# GPU lack them, and only calls on device tensors get to use either.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
 
 def _on(device: torch.device, stream, call):
