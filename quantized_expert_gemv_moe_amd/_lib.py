@@ -614,11 +614,11 @@ class Linear:
 
 
 def matmul_workspace_size(linear: Linear, max_rows: int) -> int:
-    return int(lib().moe_matmul_workspace_size(C.byref(linear.struct), int(max_rows)))
+    return int(lib().moe_matmul_workspace_size(C.byref(linear.struct), _int32("max_rows", max_rows)))
 
 
 def grouped_workspace_size(linear: Linear, max_slots: int) -> int:
-    return int(lib().moe_grouped_workspace_size(C.byref(linear.struct), int(max_slots)))
+    return int(lib().moe_grouped_workspace_size(C.byref(linear.struct), _int32("max_slots", max_slots)))
 
 
 def _alloc_bytes(n: int, device) -> Optional[torch.Tensor]:
@@ -668,6 +668,13 @@ def _strides(t: torch.Tensor, rows: int, cols: int, name: str) -> int:
 
 # The ABI's sizes are 32 bits wide, and ctypes would pass the low 32 of a longer one.
 _INT32_MAX = 0x7FFFFFFF
+
+
+def _int32(name: str, n: int) -> int:
+    n = int(n)
+    if not -_INT32_MAX <= n <= _INT32_MAX:
+        raise ValueError(f"{name} must fit 32 bits")
+    return n
 
 
 def _refuse(name: str, t: torch.Tensor, rows, cols: int, dtype, device):
@@ -790,7 +797,7 @@ def _combine(y, idx, w, n_experts, residual, out, out_dtype, handle):
     if idx.dim() != 2 or idx.dtype is not torch.int32 or not idx.is_contiguous() or idx.get_device() != index:
         raise ValueError(f"idx must be a contiguous int32 [B, k] tensor on {device}")
     B, k = idx.shape
-    if max(B, k, H, n_experts) > _INT32_MAX:
+    if max(B, k, H, n_experts) > _INT32_MAX or n_experts < -_INT32_MAX:
         raise ValueError("the sizes of y and idx and n_experts must fit 32 bits")
     if w.dtype is not torch.float32 or w.shape != idx.shape or not w.is_contiguous() or w.get_device() != index:
         _refuse("w", w, B, k, "contiguous fp32", device)
