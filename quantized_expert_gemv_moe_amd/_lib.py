@@ -571,6 +571,8 @@ class Linear:
         and kept alive by this object."""
         if activation not in _FNS:
             raise ValueError(f"activation must be one of {sorted(_FNS)}")
+        if clamp_limit > 0 and C.c_float(clamp_limit).value == 0:
+            raise ValueError("clamp_limit is too small for fp32, where it would be zero and mean none")
         if w is None or w.dim() not in (2, 3) or w.dtype not in _DTYPES or not w.is_cuda or w.numel() == 0:
             raise ValueError("w must be a non-empty [out, in] or [experts, out, in] bf16, fp16 or fp32 device tensor")
         out_dtype = w.dtype if out_dtype is None else out_dtype

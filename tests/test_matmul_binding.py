@@ -53,3 +53,9 @@ def test_combine_refuses_expert_counts_past_32_bits(n_experts):
     y, idx, w = torch.empty((0, 16)), torch.empty((0, 2), dtype=torch.int32), torch.empty((0, 2))
     with pytest.raises(ValueError, match="32 bits"):
         _lib._combine(y, idx, w, n_experts, None, None, None, 0)
+
+
+def test_linear_refuses_a_clamp_that_fp32_takes_for_none():
+    """1e-50 is zero in the descriptor's fp32, and zero means no clamp."""
+    with pytest.raises(ValueError, match="clamp_limit"):
+        moe.Linear.from_tensors(torch.zeros((4, 8)), clamp_limit=1e-50)
