@@ -209,8 +209,10 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
 
     // out overlaps nothing that the call reads, itself as the residual apart
     const int64_t row = stride_or(L->row_stride, L->in_features);
-    const int64_t group = stride_or(L->group_stride, (int64_t)L->out_features * row);
-    const int64_t bias_group = stride_or(L->bias_stride, L->out_features);
+    // one matrix has no stride to the next: any value may stand there
+    const bool one = L->n_groups == 1;
+    const int64_t group = stride_or(one ? 0 : L->group_stride, (int64_t)L->out_features * row);
+    const int64_t bias_group = stride_or(one ? 0 : L->bias_stride, L->out_features);
     const Span so{out, rows, L->out_features * (int64_t)os, os_row * (int64_t)os};
     const int64_t mat = (L->out_features - 1) * row + L->in_features;
     const Span reads[5] = {{x, x_rows, L->in_features * (int64_t)es, xs * (int64_t)es},
