@@ -45,8 +45,62 @@ static void strides_of_one_group() {
         }
 }
 
+// Rows of a and of b, s bytes apart each, that share a byte wherever their rows run on for
+// ever; counted byte by byte.
+static bool columns_meet(int64_t s, int64_t wa, int64_t wb, int64_t off) {
+    for (int64_t i = 0; i < wa; ++i)
+        for (int64_t j = 0; j < wb; ++j)
+            if ((off + j - i) % s == 0) return true;
+    return false;
+}
+
+// Columns of one buffer that do not meet are accepted, whichever comes first and
+// however many rows each has; columns that meet in a shared range are refused.
+static void columns_of_one_buffer() {
+    int accepted = 0;
+    for (int64_t s : {1, 2, 5, 8, 12})
+        for (int64_t wa = 1; wa <= s; ++wa)
+            for (int64_t wb = 1; wb <= s; ++wb)
+                for (int64_t off = -3 * s - 1; off <= 3 * s + 1; ++off)
+                    for (int64_t ra : {1, 2, 5})
+                        for (int64_t rb : {1, 3, 4}) {
+                            const char *a = (const char *)kFake, *b = a + off;
+                            const bool apart = off >= (ra - 1) * s + wa || -off >= (rb - 1) * s + wb;
+                            const bool meet = !apart && columns_meet(s, wa, wb, off);
+                            EXPECT(spans_overlap({a, ra, wa, s}, {b, rb, wb, s}) == meet);
+                            accepted += !apart && !meet;
+                        }
+    EXPECT(accepted > 1000);
+}
+
+// The same through a whole call: x and out as column ranges of one buffer of 16-bit
+// rows.
+static void calls_over_columns() {
+    int accepted = 0, refused = 0;
+    for (int64_t stride : {6, 8})
+        for (int k = 1; k <= stride; ++k)
+            for (int n = 1; n <= stride; ++n)
+                for (int64_t off = -2 * stride; off <= 2 * stride; ++off)
+                    for (int rows : {2, 3}) {
+                        const moe_linear_t L = base(k, n, MOE_DTYPE_F16);
+                        const uintptr_t x = kFake * 5, out = x + 2 * off;
+                        MatmulArgs a;
+                        MatmulChoice c;
+                        const moe_status st = prepare_matmul(&L, (const void *)x, stride, rows, 1, kRowsDense, nullptr,
+                                                             nullptr, 0, 0, (void *)out, stride, nullptr, 0, &a, &c);
+                        const bool apart = off >= (rows - 1) * stride + k || -off >= (rows - 1) * stride + n;
+                        const bool meet = !apart && columns_meet(stride, k, n, off);
+                        EXPECT(st == (meet ? MOE_ERR_INVALID_ARG : MOE_OK));
+                        accepted += !apart && !meet;
+                        refused += meet;
+                    }
+    EXPECT(accepted > 100 && refused > 100);
+}
+
 int main() {
     strides_of_one_group();
+    columns_of_one_buffer();
+    calls_over_columns();
     if (failures) return 1;
     std::printf("matmul layouts ok\n");
     return 0;
