@@ -419,10 +419,21 @@ typedef enum {
  * row_stride apart, matrices group_stride, rows of bias (and bias_up)
  * bias_stride, so gate and up may be the two halves of one stack.
  * clamp_limit (0 = none) clips z and z_up to [-L, L] before f, NaN kept.
- * Any in_features and out_features >= 1 are supported.  Pointers and strides
- * need the alignment of one element; when every base address and row is
- * 16-byte aligned and in_features fills whole 16-byte chunks, faster loads
- * are used.  MOE_ERR_UNSUPPORTED for rows of 16 MiB and more.
+ * Pointers and strides need the alignment of one element; when every base
+ * address and row is 16-byte aligned and in_features fills whole 16-byte
+ * chunks, faster loads are used.  With n_groups 1 group_stride and bias_stride
+ * are not used.
+ *
+ * Any sizes >= 1 are supported up to these limits, past which the calls return
+ * MOE_ERR_UNSUPPORTED:
+ *   rows of x, w, residual or out of 16 MiB and more (their stride, if given)
+ *   a group_stride (packed or given) or bias_stride of more than 2^40 elements
+ *   (2^30 - 1) rows or slots
+ *   work of more than 2^22 tiles; a tile is at least 64 rows of x by 64 columns of
+ *   out, 32 when gated, so a call is supported wherever
+ *     ceil(n_rows / 64) * ceil(out_features / 64 or 32) <= 2^22
+ *   with floor((n_slots + 63 * min(n_slots, n_groups)) / 64) in the place of
+ *   ceil(n_rows / 64) per expert; aligned calls go further, by larger tiles.
  */
 typedef struct {
     int32_t in_features, out_features;
@@ -501,6 +512,8 @@ moe_status moe_grouped_matmul(const moe_linear_t *linear, const void *x, int64_t
  * fp32 sums in j order, the residual added last, one rounding ("f32 partials
  * with a single final rounding", page "perf(moe): batched decode scales 1.55x
  * against 3.25x on dense", Implementation Notes).  Types are any moe_dtype.
+ * MOE_ERR_UNSUPPORTED for top_k > MOE_MAX_TOP_K, n_experts > MOE_MAX_EXPERTS,
+ * hidden >= 2^22, n_tokens * top_k >= 2^30 and n_tokens * ceil(hidden / 4) > 2^30.
  */
 moe_status moe_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx, const float *topk_w,
                        int32_t n_tokens, int32_t hidden, int32_t top_k, int32_t n_experts,

@@ -97,8 +97,65 @@ static void calls_over_columns() {
     EXPECT(accepted > 100 && refused > 100);
 }
 
+// The limits as the header states them, on both sides.  x is at an odd element's address in
+// the calls that are not aligned.
+static moe_status sized(int k, int n, int dtype, bool gated, int groups, bool aligned, int64_t rows) {
+    moe_linear_t L = base(k, n, dtype);
+    L.n_groups = groups ? groups : 1;
+    if (gated) L.w_up = (const void *)(kFake << 1);
+    moe_plan_t p;
+    std::memset(&p, 0, sizeof p);
+    p.work = (int32_t *)(kFake << 2);
+    p.sorted_slots = (int32_t *)(kFake << 3);
+    MatmulArgs a;
+    MatmulChoice c;
+    const size_t ws = groups ? moe_grouped_workspace_size(&L, (int32_t)rows) : moe_matmul_workspace_size(&L, (int32_t)rows);
+    return prepare_matmul(&L, (const void *)((kFake << 8) + (aligned ? 0 : 4)), 0, (int32_t)rows, 1,
+                          groups ? MOE_ROWS_SLOT : kRowsDense, &p, nullptr, 0, 0, (void *)(kFake << 9), 0,
+                          (void *)(kFake << 4), ws, &a, &c);
+}
+
+static void sizes_at_the_limits() {
+    const int64_t most = (int64_t)1 << 22;
+    for (int dtype : {MOE_DTYPE_F32, MOE_DTYPE_BF16})
+        for (bool gated : {false, true})
+            for (int64_t tn : {1, 3, 1000, 65535}) {
+                const int64_t cols = tn * (gated ? 32 : 64), rows = most / tn * 64;
+                for (bool aligned : {false, true}) {
+                    EXPECT(sized(64, (int)cols, dtype, gated, 0, aligned, rows) == MOE_OK);
+                    const int64_t per = rows - 63 * 100;
+                    if (per > 100) EXPECT(sized(64, (int)cols, dtype, gated, 100, aligned, per) == MOE_OK);
+                }
+                const int64_t past = (most / tn + 1) * 64;
+                EXPECT(sized(64, (int)cols, dtype, gated, 0, false, past) == MOE_ERR_UNSUPPORTED);
+            }
+    EXPECT(sized(8, 8, MOE_DTYPE_BF16, false, 0, true, ((int64_t)1 << 29)) == MOE_OK);  // tiles of 256 rows
+    EXPECT(sized(8, 8, MOE_DTYPE_BF16, false, 0, true, (int64_t)1 << 30) == MOE_ERR_UNSUPPORTED);
+    EXPECT(sized((1 << 23) - 1, 8, MOE_DTYPE_BF16, false, 0, false, 8) == MOE_OK);
+    EXPECT(sized(1 << 23, 8, MOE_DTYPE_BF16, false, 0, false, 8) == MOE_ERR_UNSUPPORTED);
+    EXPECT(sized(8, (1 << 23) - 1, MOE_DTYPE_BF16, false, 0, false, 8) == MOE_OK);
+    EXPECT(sized(8, 1 << 23, MOE_DTYPE_BF16, false, 0, false, 8) == MOE_ERR_UNSUPPORTED);
+
+    auto combine = [](int64_t tokens, int hidden, int top_k, int experts) {
+        return check_combine((const void *)kFake, MOE_DTYPE_F32, (const int32_t *)(kFake << 8), (const float *)(kFake << 9),
+                             (int32_t)tokens, hidden, top_k, experts, nullptr, 0, (const void *)(kFake << 10),
+                             MOE_DTYPE_BF16);
+    };
+    EXPECT(combine(4, 64, MOE_MAX_TOP_K, MOE_MAX_EXPERTS) == MOE_OK);
+    EXPECT(combine(4, 64, MOE_MAX_TOP_K + 1, 64) == MOE_ERR_UNSUPPORTED);
+    EXPECT(combine(4, 64, 2, MOE_MAX_EXPERTS + 1) == MOE_ERR_UNSUPPORTED);
+    EXPECT(combine(4, (1 << 22) - 1, 2, 8) == MOE_OK);
+    EXPECT(combine(4, 1 << 22, 2, 8) == MOE_ERR_UNSUPPORTED);
+    EXPECT(combine((1 << 29) - 1, 4, 2, 8) == MOE_OK);
+    EXPECT(combine(1 << 29, 4, 2, 8) == MOE_ERR_UNSUPPORTED);
+    EXPECT(combine(1 << 20, 4096, 2, 8) == MOE_OK);
+    EXPECT(combine((1 << 20) + 1, 4096, 2, 8) == MOE_ERR_UNSUPPORTED);
+    EXPECT(combine(1 << 20, 4097, 2, 8) == MOE_ERR_UNSUPPORTED);
+}
+
 int main() {
     strides_of_one_group();
+    sizes_at_the_limits();
     columns_of_one_buffer();
     calls_over_columns();
     if (failures) return 1;
