@@ -391,7 +391,8 @@ moe_status moe_layer_check(const moe_layer_t *layer);
  * gather", Proposed Solution step 2).
  */
 
-/* f of the epilogue; z is the fp32 sum x.w plus bias. */
+/* f of the epilogue; z is the fp32 sum x.w plus bias.  Factors of z below the smallest
+ * normal fp32 value (a SiLU of z < -87.3) may count as zero. */
 typedef enum {
     MOE_FN_NONE = 0,
     MOE_FN_RELU = 1,      /* max(z, 0), NaN kept */

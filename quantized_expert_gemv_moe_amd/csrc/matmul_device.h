@@ -231,7 +231,8 @@ __device__ __forceinline__ float clip(float z, float limit) {  // NaN stays NaN
 
 // z / (1 + exp(-a)).  The exponential is 2 to the rounded product -a log2(e): off by |a|
 // 2^-24 relative where it counts, which is below the rounding of 16-bit outputs and
-// next to that of the products' sums in fp32.  The reciprocal is good to 1 ulp.
+// next to that of the products' sums in fp32.  The reciprocal is good to 1 ulp; below
+// 2^-126 it is zero, so f counts as zero from a = -87.3 down (1e-36 and less).
 __device__ __forceinline__ float sigmoid_mul(float z, float a) {
     return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.4426950408889634f));
 }

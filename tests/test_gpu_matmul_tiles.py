@@ -124,3 +124,17 @@ def test_gathered_rows_just_below_4_gib(case, rows):
     for e in range(E):
         mine = torch.nonzero(idx[:, 0] == e)[:, 0]
         ref.check(out[mine], *ref.product(x[mine], lin.w[e], out_dtype=BF16), f"{case} e={e}")
+
+
+def test_functions_where_their_factor_underflows():
+    """Far below zero f(z) = z times a factor below the normal range, which may count as zero;
+    nothing else is lost on the way there."""
+    log("[case] functions below -40")
+    z = torch.linspace(-140, -6, 4001, device="cuda")
+    x = z[:, None].contiguous()
+    w = torch.ones((1, 1), device="cuda")
+    for act in ("silu", "gelu", "gelu_tanh"):
+        out = moe.matmul(moe.Linear.from_tensors(w, activation=act), x)
+        torch.cuda.synchronize()
+        want, tol = ref.product(x, w, act=act)
+        ref.check(out, want, tol + z.double().abs()[:, None] * 2.0 ** -126, act)
