@@ -103,10 +103,17 @@ static const Cost kCosts[] = {
     {kMatmulFew, 2, 0, 2.7, 0.0, 0.170, 0.170}};
 
 // K in stretches (kMatmulDeep): at most 16 of them, at most one tile's stretch for
-// each CU, and only where the model says that it gains more than the join costs: 3 us
-// on the device, and a second launch's 4 us on the host when calls are enqueued one by
-// one.  bf16, K 8192: 16 rows, N 512 17.7 (kernel for few rows) -> 8.1 us; 64 rows, N
-// 2048 24.6 -> 18.8 us; 16 rows, N 2048 17.7 either way, not split.
+// each CU, and only where the model says that it gains more than kJoinCost, in us: 3 on
+// the device for the join, 4 on the host for its launch, and 1.5 of margin.  The host's
+// part is for calls that are enqueued one by one; calls replayed from a graph do not pay it,
+// and keep one launch where stretches would be faster.  bf16, weights from HBM, one launch and
+// as the rule has it:
+//   16 rows, K 8192, N 512    kernel for few rows 16.4, sixteen stretches of 32 x 64 9.1
+//   64 rows, K 8192, N 2048   kernel for few rows 26.6, eight stretches of 64 x 128 18.9
+//   16 rows, K 8192, N 2048   17.5 and 17.8: nothing gained; the model puts 64 x 128 first, but
+//                             eight stretches of 32 x 64 take 13.6
+//   64 rows, K 4096, N 2048   kernel for few rows 14.7, which is taken; four stretches of
+//                             32 x 64 take 11.0
 constexpr int kMaxSplits = 16;
 constexpr int64_t kMaxSplitTiles = 256;
 constexpr double kJoinCost = 8.5;
@@ -133,8 +140,11 @@ MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bo
         const double rounds = n <= 256 ? 1 : (double)(int64_t)((n + 255) / 256);
         double step = n <= 256 && k.alone > k.step ? k.alone : n <= 128 ? k.alone : k.step * rounds;
         if (f32 && !few) step *= 3;
-        // experts that fill less than half of the largest tile (256 experts of 96 rows, 4096
-        // -> 2048 gated: 256 x 256 1836, 128 x 128 1670 us; 128 of 128 rows: 183 and 207 us)
+        // experts that fill less than half of the largest tile.  128 x 128 and 256 x 256, gated, at
+        // 64, 96, 128 and 160 rows an expert:
+        //   256 experts, 4096 -> 2048   1585 1678 2084 2373   1822 1838 1881 1889 us
+        //   128 experts, 2048 -> 768     149  158  207  219    165  167  172  176
+        //    64 experts, 1024 -> 1024     50   54   72   80     66   70   67   69
         if (grouped && k.mt == 8 && rows < 128 * used) step *= 1.15;
         if (few && gated && k.mt == 2) step *= 1.4;
         if (few && !is_aligned) step *= 2.3;
