@@ -209,15 +209,15 @@ def prepare(case, seed):
                                      n_groups=case["groups"], top_groups=case["keep"], group_score=case["by"],
                                      renormalise=case["renorm"], scale=case["scale"])
             return s
-        s["linear"] = moe.LinearI8.from_tensors(s["w"], s["w_scale"], bias=s["bias"], w_up=s["w_up"],
+        s["linear"] = moe.LinearInt.from_tensors(s["w"], s["w_scale"], bias=s["bias"], w_up=s["w_up"],
                                                 w_up_scale=s["w_up_scale"], bias_up=s["bias_up"],
                                                 activation=case["act"], out_dtype=_DTYPES[case["out"]],
                                                 clamp_limit=case["clamp"])
         if case["op"] == "dense":
-            s["workspace"] = moe.alloc_matmul_i8_workspace(s["linear"], case["rows"])
+            s["workspace"] = moe.alloc_matmul_int_workspace(s["linear"], case["rows"])
         else:
             s["plan"] = moe.expert_plan(s["idx"], case["experts"])
-            s["workspace"] = moe.alloc_grouped_i8_workspace(s["linear"], s["idx"].numel(), s["x"].shape[0])
+            s["workspace"] = moe.alloc_grouped_int_workspace(s["linear"], s["idx"].numel(), s["x"].shape[0])
     return s
 
 
@@ -232,9 +232,9 @@ def run(state):
             idx, w, p = moe.router_plan(state["router"], state["logits"])
             return idx, w, [p.counts, p.offsets, p.sorted_slots, p.unique_experts, p.n_unique, p.work]
         if c["op"] == "dense":
-            return moe.matmul_i8(state["linear"], state["x"], x_scale=state["x_scale"], residual=state["residual"],
+            return moe.matmul_int(state["linear"], state["x"], x_scale=state["x_scale"], residual=state["residual"],
                                  out=state["out"], workspace=state["workspace"])
-        return moe.grouped_matmul_i8(state["linear"], state["x"], state["plan"], c["tokens"] * c["top_k"],
+        return moe.grouped_matmul_int(state["linear"], state["x"], state["plan"], c["tokens"] * c["top_k"],
                                      top_k=c["top_k"], rows=c["rows"], x_scale=state["x_scale"], out=state["out"],
                                      workspace=state["workspace"])
     if c["op"] == "route":
