@@ -56,9 +56,11 @@ typedef enum {
     MOE_ERR_DEVICE = 4
 } moe_status;
 
-/* MOE_DTYPE_F16 is a type of the unquantised products (moe_linear_t) and of
- * moe_combine only; the quantised layer and the router projection refuse it. */
-typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2 } moe_dtype;
+/* MOE_DTYPE_F16 is a type of the unquantised products (moe_linear_t), of
+ * moe_combine, of the scored router and of the integer products; the quantised layer and
+ * the router projection refuse it.  MOE_DTYPE_I8 is a type of x of the integer
+ * products (moe_matmul_int, moe_grouped_matmul_int) only. */
+typedef enum { MOE_DTYPE_F32 = 0, MOE_DTYPE_BF16 = 1, MOE_DTYPE_F16 = 2, MOE_DTYPE_I8 = 3 } moe_dtype;
 
 /* Storage of the down projection (see moe_layer_t and moe_pack_down). */
 typedef enum { MOE_DOWN_ROWS = 0, MOE_DOWN_COLS = 1 } moe_down_layout;
@@ -520,6 +522,155 @@ moe_status moe_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx, 
                        int32_t n_tokens, int32_t hidden, int32_t top_k, int32_t n_experts,
                        const void *residual, int32_t residual_dtype, void *out, int32_t out_dtype,
                        void *hip_stream);
+
+/* ------------------------------------------------------- scored routing
+ *
+ * The router (page "perf(moe): attribute the MoE decode gap at the M = 1 expert gather",
+ * Proposed Solution step 2) of models whose scores are not the softmax of the kept
+ * logits: softmax over all experts or sigmoid scores, a bias for balance that
+ * only the choice sees, groups of experts of which the best are kept, weights
+ * renormalised or not and scaled.
+ */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+/* What a group of experts is ranked by: its best c, or the sum of its two best. */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+
+#define MOE_MAX_GROUPS 64
+
+/*
+ * A router, in host memory; bias is a device pointer.  With the logits l of a token:
+ *   s = softmax(l) over all experts, or sigmoid(l)
+ *   c = s + bias, in 64 bits.  Without a bias experts are in the order of l itself,
+ *       in which s rises.  Scores too small for 64 bits (a sigmoid of l < -709) are zero.
+ * An expert is masked when its logit is -infinity or the lowest finite value of the logits'
+ * type, or its bias is -infinity.  The softmax leaves out experts masked by their logits.
+ *   Of n_groups groups of n_experts / n_groups consecutive experts the top_groups best are
+ *   kept, by their best unmasked c (l without a bias) or by the sum of their two best
+ *   (one where it has one), ties to the lower group, groups without an unmasked expert last.
+ *   Of the kept groups' experts the top_k of largest c are chosen, in that order, ties to the
+ *   lower expert id, masked ones after all others.
+ *   w = s of the chosen, 0 for a masked one; renormalise: divided by their sum (left 0
+ *       where that is 0); times scale; rounded once to fp32.
+ * A token's ids are -1 and its weights NaN if any unmasked expert's logit is NaN, or
+ * +infinity under softmax, or its bias is NaN or +infinity: the planner leaves the
+ * token out and the combine makes it NaN.
+ */
+typedef struct {
+    int32_t n_experts;   /* 1..MOE_MAX_EXPERTS */
+    int32_t top_k;       /* 1..MOE_MAX_TOP_K, at most the kept groups' experts */
+    int32_t score;       /* moe_score */
+    int32_t n_groups;    /* 1..MOE_MAX_GROUPS, divides n_experts; 1 = no groups */
+    int32_t top_groups;  /* 1..n_groups */
+    int32_t group_score; /* moe_group_score */
+    int32_t renormalise; /* 0 or 1 */
+    float scale;         /* finite, > 0 */
+    const float *bias;   /* [n_experts] or NULL */
+} moe_router_t;
+
+/* Host-only check of a router (no device access). */
+moe_status moe_router_check(const moe_router_t *router);
+
+/*
+ * Routes a batch.
+ *   logits    [n_tokens][n_experts] of logits_dtype (fp32, bf16 or fp16), rows
+ *             logits_stride elements apart (0 = packed)
+ *   topk_idx  int32 [n_tokens][top_k], topk_w fp32 [n_tokens][top_k], packed: what
+ *             moe_expert_plan, moe_decode_step and moe_combine take
+ * Outputs must not overlap one another or the inputs.  A token's result depends on its
+ * logits alone.  n_tokens == 0 returns MOE_OK without a launch.
+ */
+moe_status moe_router_topk(const moe_router_t *router, const void *logits, int32_t logits_dtype,
+                           int64_t logits_stride, int32_t n_tokens, int32_t *topk_idx, float *topk_w,
+                           void *hip_stream);
+
+/* moe_router_topk, then moe_expert_plan of its choice: one launch for up to 16 tokens.
+ * n_tokens == 0 writes an empty plan. */
+moe_status moe_router_plan(const moe_router_t *router, const void *logits, int32_t logits_dtype,
+                           int64_t logits_stride, int32_t n_tokens, int32_t *topk_idx, float *topk_w,
+                           const moe_plan_t *plan, void *hip_stream);
+
+/* ----------------------------------------------- 8-bit integer products
+ *
+ * Layers and experts whose weights are 8-bit integers with a scale for each output
+ * channel, on activations that are 8-bit integers with a scale for each row: the products
+ * of moe_matmul and moe_grouped_matmul on the matrix cores' integer instructions, with the
+ * same epilogue, plans and rows.  Activations may be given in fp32, bf16 or fp16; the
+ * call then quantises their rows as moe_quantize_rows does.
+ */
+
+/*
+ * codes[r][c] = x[r][c] * 127 / max |x[r]| rounded to the nearest integer, ties to the even one
+ * (of the exact quotient), scales[r] = max |x[r]| / 127 rounded to fp32, so that
+ * x ~ codes * scales.  A row of zeros has codes and scale 0; a row that holds an
+ * infinity or NaN has codes 0 and scale NaN.
+ *   x       [n_rows][n_cols] of dtype (fp32, bf16, fp16), rows x_stride elements apart
+ *   codes   int8 [n_rows][n_cols], rows codes_stride apart
+ *   scales  fp32 [n_rows]
+ * Strides of 0 mean packed rows.  codes and scales must not overlap one another or x.
+ * The same call makes weights: a row for each output channel.
+ * MOE_ERR_UNSUPPORTED for rows (strides) of 16 MiB and more, or 2^30 rows and more.
+ */
+moe_status moe_quantize_rows(const void *x, int32_t dtype, int64_t x_stride, int32_t n_rows, int32_t n_cols,
+                             int8_t *codes, int64_t codes_stride, float *scales, void *hip_stream);
+
+/*
+ * Integer weights of a product, in host memory, its pointers device pointers; as
+ * moe_linear_t, with
+ *   w          int8 [n_groups][out_features][in_features], w_scale fp32 [n_groups][out_features]
+ *   w_up, w_up_scale  both or neither: the gated product's second stack
+ *   bias, bias_up     [n_groups][out_features] of bias_dtype (fp32, bf16, fp16)
+ * row_tail bytes behind each row's in_features belong to the same buffer and are zero
+ * (0 = none are known to be): rows whose in_features and row_tail together fill
+ * whole 16-byte chunks, at 16-byte addresses, take the faster loads.  in_features is at most
+ * MOE_MAX_I8_INPUTS, for which the sums fit 32 bits whatever the integers; beyond it, and
+ * beyond moe_linear_t's other limits, MOE_ERR_UNSUPPORTED.
+ */
+#define MOE_MAX_I8_INPUTS 131071
+typedef struct {
+    int32_t in_features, out_features;
+    int32_t n_groups;
+    int32_t out_dtype;    /* moe_dtype of out: fp32, bf16, fp16 */
+    int32_t fn;           /* moe_fn */
+    float clamp_limit;    /* >= 0; 0 = none */
+    int32_t bias_dtype;
+    int32_t row_tail;     /* 0..15 */
+    const int8_t *w, *w_up;
+    const float *w_scale, *w_up_scale;
+    const void *bias, *bias_up;
+    int64_t row_stride, group_stride, scale_stride, bias_stride; /* elements; 0 = packed */
+} moe_linear_int_t;
+
+/* Host-only check of a descriptor (no device access). */
+moe_status moe_linear_int_check(const moe_linear_int_t *linear);
+
+/* Bytes of device workspace for up to max_rows rows, or max_slots slots over at most
+ * max_x_rows rows of x, of any type of x; 0 if the descriptor or a number is invalid. */
+size_t moe_matmul_int_workspace_size(const moe_linear_int_t *linear, int32_t max_rows);
+size_t moe_grouped_int_workspace_size(const moe_linear_int_t *linear, int32_t max_slots, int32_t max_x_rows);
+
+/*
+ * out[r] = residual[r] + f(z),  z = x_scale[r] * w_scale * sum_k x[r][k] w[k] + bias
+ * (f(z) * z_up when gated).
+ *   x         x_dtype MOE_DTYPE_I8: int8 [n_rows][in_features] with x_scale fp32 [n_rows]
+ *             x_dtype fp32, bf16 or fp16: quantised within the call; x_scale is NULL
+ *   workspace moe_matmul_int_workspace_size(linear, n_rows) bytes, 256-byte aligned; contents
+ *             need no initialisation.  Calls that may overlap in time need one each.
+ *             A call that needs less takes less (none: NULL will do).
+ * The integer sum is exact; it, the two scales' product and their product are rounded to
+ * fp32 once each, what follows is as in moe_matmul.  Repeated calls are bitwise equal.
+ */
+moe_status moe_matmul_int(const moe_linear_int_t *linear, const void *x, int32_t x_dtype, int64_t x_stride,
+                         const float *x_scale, int32_t n_rows, const void *residual, int32_t residual_dtype,
+                         int64_t residual_stride, void *out, int64_t out_stride, void *workspace,
+                         size_t workspace_bytes, void *hip_stream);
+
+/* The same for every expert of a planned batch: moe_grouped_matmul with integer operands.
+ * x and x_scale have a row per token or slot, or a sorted row, as `rows` says. */
+moe_status moe_grouped_matmul_int(const moe_linear_int_t *linear, const void *x, int32_t x_dtype, int64_t x_stride,
+                                 const float *x_scale, int32_t n_slots, int32_t top_k, int32_t rows,
+                                 const moe_plan_t *plan, void *out, int64_t out_stride, void *workspace,
+                                 size_t workspace_bytes, void *hip_stream);
 
 /* Static description of a status code. */
 const char *moe_status_str(moe_status status);

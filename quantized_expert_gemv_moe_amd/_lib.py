@@ -18,7 +18,7 @@ import torch
 from . import build as _build
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_DEVICE = range(5)
-MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16 = 0, 1, 2
+MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_I8 = 0, 1, 2, 3
 MOE_DOWN_ROWS, MOE_DOWN_COLS = 0, 1
 MOE_ACT_SWIGLU, MOE_ACT_GEGLU = 0, 1
 _ACTIVATIONS = {"swiglu": MOE_ACT_SWIGLU, "geglu": MOE_ACT_GEGLU}
@@ -28,7 +28,13 @@ _FNS = {"none": MOE_FN_NONE, "relu": MOE_FN_RELU, "silu": MOE_FN_SILU, "gelu": M
 MOE_ROWS_TOKEN, MOE_ROWS_SLOT, MOE_ROWS_SORTED = range(3)
 _ROWS = {"token": MOE_ROWS_TOKEN, "slot": MOE_ROWS_SLOT, "sorted": MOE_ROWS_SORTED}
 _DTYPES = {torch.float32: MOE_DTYPE_F32, torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16}
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+_GROUP_SCORES = {"max": MOE_GROUP_MAX, "top2": MOE_GROUP_TOP2}
 MOE_MAX_EXPERTS = 1024
+MOE_MAX_GROUPS = 64
+MOE_MAX_I8_INPUTS = 131071
 MOE_MAX_TOP_K = 16
 MOE_MAX_TOKENS = 65535
 MOE_STATIC_SCRATCH_BYTES = 8 << 20
@@ -68,6 +74,25 @@ class LinearStruct(C.Structure):
     ]
 
 
+class RouterStruct(C.Structure):
+    _fields_ = [
+        ("n_experts", C.c_int32), ("top_k", C.c_int32), ("score", C.c_int32), ("n_groups", C.c_int32),
+        ("top_groups", C.c_int32), ("group_score", C.c_int32), ("renormalise", C.c_int32), ("scale", C.c_float),
+        ("bias", C.c_void_p),
+    ]
+
+
+class LinearIntStruct(C.Structure):
+    _fields_ = [
+        ("in_features", C.c_int32), ("out_features", C.c_int32), ("n_groups", C.c_int32), ("out_dtype", C.c_int32),
+        ("fn", C.c_int32), ("clamp_limit", C.c_float), ("bias_dtype", C.c_int32), ("row_tail", C.c_int32),
+        ("w", C.c_void_p), ("w_up", C.c_void_p), ("w_scale", C.c_void_p), ("w_up_scale", C.c_void_p),
+        ("bias", C.c_void_p), ("bias_up", C.c_void_p),
+        ("row_stride", C.c_int64), ("group_stride", C.c_int64), ("scale_stride", C.c_int64),
+        ("bias_stride", C.c_int64),
+    ]
+
+
 _lib = None
 
 EXPORTS = ("moe_router_logits", "moe_route_topk", "moe_expert_plan", "moe_route_plan", "moe_workspace_size",
@@ -75,7 +100,9 @@ EXPORTS = ("moe_router_logits", "moe_route_topk", "moe_expert_plan", "moe_route_
            "moe_decode_layer", "moe_decode_layer_static", "moe_route_gate_up", "moe_expert_gate_up", "moe_expert_down_combine", "moe_pack_down",
            "moe_layer_check", "moe_status_str", "moe_abi_version",
            "moe_linear_check", "moe_matmul_workspace_size", "moe_grouped_workspace_size", "moe_matmul",
-           "moe_grouped_matmul", "moe_combine")
+           "moe_grouped_matmul", "moe_combine", "moe_router_check", "moe_router_topk", "moe_router_plan",
+           "moe_quantize_rows", "moe_linear_int_check", "moe_matmul_int_workspace_size",
+           "moe_grouped_int_workspace_size", "moe_matmul_int", "moe_grouped_matmul_int")
 
 
 def library_path() -> str:
@@ -142,6 +169,26 @@ def lib() -> C.CDLL:
         L.moe_grouped_matmul.restype = C.c_int
         L.moe_combine.argtypes = [vp, i32, vp, vp, i32, i32, i32, i32, vp, i32, vp, i32, vp]
         L.moe_combine.restype = C.c_int
+        rp, qp = C.POINTER(RouterStruct), C.POINTER(LinearIntStruct)
+        L.moe_router_check.argtypes = [rp]
+        L.moe_router_check.restype = C.c_int
+        L.moe_router_topk.argtypes = [rp, vp, i32, i64, i32, vp, vp, vp]
+        L.moe_router_topk.restype = C.c_int
+        L.moe_router_plan.argtypes = [rp, vp, i32, i64, i32, vp, vp, C.POINTER(PlanStruct), vp]
+        L.moe_router_plan.restype = C.c_int
+        L.moe_quantize_rows.argtypes = [vp, i32, i64, i32, i32, vp, i64, vp, vp]
+        L.moe_quantize_rows.restype = C.c_int
+        L.moe_linear_int_check.argtypes = [qp]
+        L.moe_linear_int_check.restype = C.c_int
+        L.moe_matmul_int_workspace_size.argtypes = [qp, i32]
+        L.moe_matmul_int_workspace_size.restype = C.c_size_t
+        L.moe_grouped_int_workspace_size.argtypes = [qp, i32, i32]
+        L.moe_grouped_int_workspace_size.restype = C.c_size_t
+        L.moe_matmul_int.argtypes = [qp, vp, i32, i64, vp, i32, vp, i32, i64, vp, i64, vp, C.c_size_t, vp]
+        L.moe_matmul_int.restype = C.c_int
+        L.moe_grouped_matmul_int.argtypes = [qp, vp, i32, i64, vp, i32, i32, i32, C.POINTER(PlanStruct), vp, i64, vp,
+                                            C.c_size_t, vp]
+        L.moe_grouped_matmul_int.restype = C.c_int
         L.moe_status_str.argtypes = [C.c_int]
         L.moe_status_str.restype = C.c_char_p
         L.moe_abi_version.argtypes = []
@@ -823,4 +870,376 @@ def _combine(y, idx, w, n_experts, residual, out, out_dtype, handle):
                            out.data_ptr(), out_type, handle)
     if st:
         raise MoeError(st, "moe_combine")
+    return out
+
+
+# ---------------------------------------------------------- scored routing
+@dataclass
+class Router:
+    """Router of scored experts plus the ABI descriptor (moe_router_t).
+
+    ``score``: "softmax" (over all experts) or "sigmoid".  ``bias``: fp32 [n_experts] device tensor
+    that is added to the scores for the choice only; it is used in place and kept alive by
+    this object.  ``n_groups`` groups of consecutive experts, of which the ``top_groups`` best by
+    ``group_score`` ("max", or "top2": the sum of the two best) are kept.  ``renormalise``: the
+    chosen experts' weights are divided by their sum.  ``scale`` multiplies them."""
+
+    n_experts: int
+    top_k: int
+    score: str = "softmax"
+    bias: Optional[torch.Tensor] = None
+    n_groups: int = 1
+    top_groups: int = 1
+    group_score: str = "max"
+    renormalise: bool = True
+    scale: float = 1.0
+
+    def __post_init__(self):
+        if self.score not in _SCORES:
+            raise ValueError(f"score must be one of {sorted(_SCORES)}")
+        if self.group_score not in _GROUP_SCORES:
+            raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORES)}")
+        sizes = [_int32(n, getattr(self, n)) for n in ("n_experts", "top_k", "n_groups", "top_groups")]
+        b = self.bias
+        if b is not None and (b.dtype is not torch.float32 or b.shape != (sizes[0],) or not b.is_contiguous()
+                              or not b.is_cuda):
+            raise ValueError(f"bias must be a contiguous fp32 [{sizes[0]}] device tensor")
+        self.struct = RouterStruct(n_experts=sizes[0], top_k=sizes[1], score=_SCORES[self.score], n_groups=sizes[2],
+                                   top_groups=sizes[3], group_score=_GROUP_SCORES[self.group_score],
+                                   renormalise=int(bool(self.renormalise)), scale=float(self.scale),
+                                   bias=None if b is None else b.data_ptr())
+        self.index = None if b is None else b.get_device()
+        self._ref = C.byref(self.struct)
+        _check(self.check(), "moe_router_check")
+
+    def check(self) -> int:
+        return lib().moe_router_check(C.byref(self.struct))
+
+
+def router_topk(router: Router, logits: torch.Tensor, idx: Optional[torch.Tensor] = None,
+                w: Optional[torch.Tensor] = None, stream=None):
+    """moe_router_topk: logits [B, E] (fp32, bf16 or fp16, rows may be strided) -> (int32 idx [B, k],
+    fp32 w [B, k])."""
+    index = logits.get_device()
+    if index < 0:
+        raise ValueError("logits must be a device tensor")
+    if stream is not None or _get_device() != index:
+        return _on(logits.device, stream, lambda handle: _router(router, logits, None, False, idx, w, handle))
+    return _router(router, logits, None, False, idx, w, _raw_stream(index))
+
+
+def router_plan(router: Router, logits: torch.Tensor, plan: Optional[Plan] = None,
+                idx: Optional[torch.Tensor] = None, w: Optional[torch.Tensor] = None, stream=None):
+    """moe_router_plan: the router and the planner of its choice; returns (idx, w, plan)."""
+    index = logits.get_device()
+    if index < 0:
+        raise ValueError("logits must be a device tensor")
+    if stream is not None or _get_device() != index:
+        return _on(logits.device, stream, lambda handle: _router(router, logits, plan, True, idx, w, handle))
+    return _router(router, logits, plan, True, idx, w, _raw_stream(index))
+
+
+def _router(router, logits, plan, planned, idx, w, handle):
+    device, index, E, k = logits.device, logits.get_device(), router.struct.n_experts, router.struct.top_k
+    dtype = _DTYPES.get(logits.dtype)
+    if logits.dim() != 2 or logits.shape[1] != E or dtype is None:
+        _refuse("logits", logits, "B", E, "fp32, bf16 or fp16", device)
+    if router.index is not None and router.index != index:
+        raise ValueError(f"the router's bias is on device {router.index}, the logits on {device}")
+    B = logits.shape[0]
+    if B > _INT32_MAX:
+        raise ValueError(f"logits has {B} rows, more than fit 32 bits")
+    if idx is None:
+        idx = torch.empty((B, k), dtype=torch.int32, device=device)
+    elif idx.shape != (B, k) or idx.dtype is not torch.int32 or not idx.is_contiguous() or idx.get_device() != index:
+        _refuse("idx", idx, B, k, "contiguous int32", device)
+    if w is None:
+        w = torch.empty((B, k), dtype=torch.float32, device=device)
+    elif w.shape != (B, k) or w.dtype is not torch.float32 or not w.is_contiguous() or w.get_device() != index:
+        _refuse("w", w, B, k, "contiguous fp32", device)
+    stride = _strides(logits, B, E, "logits")
+    if not planned:
+        st = lib().moe_router_topk(router._ref, logits.data_ptr(), dtype, stride, B, idx.data_ptr(), w.data_ptr(), handle)
+        if st:
+            raise MoeError(st, "moe_router_topk")
+        return idx, w
+    if plan is None:
+        plan = Plan.allocate(E, B * k, device=device)
+    else:
+        _check_plan_buffers(plan, E, B * k)
+        if plan.work.get_device() != index:
+            raise ValueError(f"the plan is not on {device}")
+    st = lib().moe_router_plan(router._ref, logits.data_ptr(), dtype, stride, B, idx.data_ptr(), w.data_ptr(),
+                               C.byref(plan.struct), handle)
+    if st:
+        raise MoeError(st, "moe_router_plan")
+    return idx, w, plan
+
+
+# --------------------------------------------------- 8-bit integer products
+def quantize_rows(x: torch.Tensor, codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                  stream=None):
+    """moe_quantize_rows: x [rows, cols] (fp32, bf16 or fp16, rows may be strided) -> (int8 codes
+    [rows, cols], fp32 scales [rows]) with x ~ codes * scales[:, None]."""
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("x must be a device tensor")
+    if stream is not None or _get_device() != index:
+        return _on(x.device, stream, lambda handle: _quantize(x, codes, scales, handle))
+    return _quantize(x, codes, scales, _raw_stream(index))
+
+
+def _quantize(x, codes, scales, handle):
+    device, index, dtype = x.device, x.get_device(), _DTYPES.get(x.dtype)
+    if x.dim() != 2 or dtype is None:
+        raise ValueError("x must be a bf16, fp16 or fp32 [rows, cols] tensor")
+    rows, cols = x.shape
+    if max(rows, cols) > _INT32_MAX:
+        raise ValueError("the sizes of x must fit 32 bits")
+    if codes is None:
+        codes = torch.empty((rows, cols), dtype=torch.int8, device=device)
+    elif codes.shape != x.shape or codes.dtype is not torch.int8 or codes.get_device() != index:
+        _refuse("codes", codes, rows, cols, torch.int8, device)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=device)
+    elif (scales.shape != (rows,) or scales.dtype is not torch.float32 or not scales.is_contiguous()
+          or scales.get_device() != index):
+        raise ValueError(f"scales must be a contiguous fp32 [{rows}] tensor on {device}")
+    st = lib().moe_quantize_rows(x.data_ptr(), dtype, _strides(x, rows, cols, "x"), rows, cols, codes.data_ptr(),
+                                 _strides(codes, rows, cols, "codes"), scales.data_ptr(), handle)
+    if st:
+        raise MoeError(st, "moe_quantize_rows")
+    return codes, scales
+
+
+def _whole_chunks(w: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """w with rows of whole 16-byte chunks at 16-byte addresses: itself, or a copy whose rows are
+    followed by zeros."""
+    if w is None:
+        return None
+    K = w.shape[-1]
+    strides = [s for n, s in zip(w.shape[:-1], w.stride()[:-1]) if n > 1]
+    if K % 16 == 0 and w.data_ptr() % 16 == 0 and all(s % 16 == 0 for s in strides):
+        return w
+    wide = torch.zeros((*w.shape[:-1], (K + 15) // 16 * 16), dtype=torch.int8, device=w.device)
+    wide[..., :K] = w
+    return wide[..., :K]
+
+
+@dataclass
+class LinearInt:
+    """Integer weights of a product plus the ABI descriptor (moe_linear_int_t) pointing at them."""
+
+    w: torch.Tensor
+    w_scale: torch.Tensor
+    w_up: Optional[torch.Tensor]
+    w_up_scale: Optional[torch.Tensor]
+    bias: Optional[torch.Tensor]
+    bias_up: Optional[torch.Tensor]
+    in_features: int
+    out_features: int
+    n_groups: int
+    out_dtype: torch.dtype
+    struct: LinearIntStruct
+
+    def __post_init__(self):
+        self.device, self.index = self.w.device, self.w.get_device()
+        self._ref = C.byref(self.struct)
+
+    @staticmethod
+    def from_tensors(w: torch.Tensor, w_scale: torch.Tensor, bias: Optional[torch.Tensor] = None,
+                     w_up: Optional[torch.Tensor] = None, w_up_scale: Optional[torch.Tensor] = None,
+                     bias_up: Optional[torch.Tensor] = None, activation: str = "none",
+                     out_dtype: torch.dtype = torch.bfloat16, clamp_limit: float = 0.0) -> "LinearInt":
+        """``w``: int8 [out, in], or [experts, out, in] for grouped_matmul_int, each row contiguous, with
+        ``w_scale``: fp32 [out] or [experts, out]; ``w_up`` and ``w_up_scale`` (same shapes and
+        strides) make the product gated.  ``bias`` and ``bias_up``: [out] or [experts, out], bf16, fp16
+        or fp32.  ``activation``: none, relu, silu, gelu or gelu_tanh.  The tensors are used in
+        place and kept alive by this object, but for weights whose rows do not fill whole 16-byte
+        chunks at 16-byte addresses: those are copied once, here, into rows that do."""
+        if activation not in _FNS:
+            raise ValueError(f"activation must be one of {sorted(_FNS)}")
+        if clamp_limit > 0 and C.c_float(clamp_limit).value == 0:
+            raise ValueError("clamp_limit is too small for fp32, where it would be zero and mean none")
+        if w is None or w.dim() not in (2, 3) or w.dtype is not torch.int8 or not w.is_cuda or w.numel() == 0:
+            raise ValueError("w must be a non-empty int8 [out, in] or [experts, out, in] device tensor")
+        if out_dtype not in _DTYPES:
+            raise ValueError("out_dtype must be bf16, fp16 or fp32")
+        if (w_up is None) != (w_up_scale is None) or (bias_up is not None) != (bias is not None and w_up is not None):
+            raise ValueError("w_up and w_up_scale go together, and bias_up goes with bias and w_up")
+        N, K = w.shape[-2:]
+        E = w.shape[0] if w.dim() == 3 else 1
+        if max(N, K, E) > _INT32_MAX:
+            raise ValueError("the sizes of w must fit 32 bits")
+        if w_up is not None and (w_up.shape != w.shape or w_up.dtype is not w.dtype or w_up.device != w.device):
+            raise ValueError("w_up must match w in shape, type and device")
+        for t in (w, w_up):
+            if t is not None and K > 1 and t.stride(-1) != 1:
+                raise ValueError("the rows of w and w_up must be contiguous")
+            if t is not None and ((N > 1 and t.stride(-2) < K) or (E > 1 and t.stride(0) <= 0)):
+                raise ValueError("expanded (broadcast) weights have no layout here")
+
+        def rows(t, like, name, types):
+            if t is None:
+                return
+            if t.shape != w.shape[:-1] or t.dtype not in types or t.device != w.device or (N > 1 and t.stride(-1) != 1):
+                raise ValueError(f"{name} must be [out] or [experts, out] on w's device, rows contiguous")
+            if t.dtype is not like.dtype or (E > 1 and (t.stride(0) != like.stride(0) or t.stride(0) < N)):
+                raise ValueError(f"{name} must not be expanded, and matches its partner in type and strides")
+
+        rows(w_scale, w_scale, "w_scale", (torch.float32,))
+        rows(w_up_scale, w_scale, "w_up_scale", (torch.float32,))
+        rows(bias, bias, "bias", _DTYPES)
+        rows(bias_up, bias, "bias_up", _DTYPES)
+        w, w_up = _whole_chunks(w), _whole_chunks(w_up)
+        if w_up is not None and any(n > 1 and a != b for n, a, b in zip(w.shape, w.stride(), w_up.stride())):
+            w, w_up = w.contiguous(), w_up.contiguous()
+            w, w_up = _whole_chunks(w), _whole_chunks(w_up)
+        tail = -K % 16
+        row = w.stride(-2) if N > 1 else K + tail
+        group = w.stride(0) if E > 1 else 0
+        st = LinearIntStruct(in_features=K, out_features=N, n_groups=E, out_dtype=_DTYPES[out_dtype],
+                            fn=_FNS[activation], clamp_limit=float(clamp_limit),
+                            bias_dtype=MOE_DTYPE_F32 if bias is None else _DTYPES[bias.dtype], row_tail=tail,
+                            w=w.data_ptr(), w_up=None if w_up is None else w_up.data_ptr(), w_scale=w_scale.data_ptr(),
+                            w_up_scale=None if w_up_scale is None else w_up_scale.data_ptr(),
+                            bias=None if bias is None else bias.data_ptr(),
+                            bias_up=None if bias_up is None else bias_up.data_ptr(),
+                            row_stride=row, group_stride=group, scale_stride=w_scale.stride(0) if E > 1 else 0,
+                            bias_stride=bias.stride(0) if bias is not None and E > 1 else 0)
+        lin = LinearInt(w, w_scale, w_up, w_up_scale, bias, bias_up, K, N, E, out_dtype, st)
+        _check(lin.check(), "moe_linear_int_check")
+        return lin
+
+    def check(self) -> int:
+        return lib().moe_linear_int_check(C.byref(self.struct))
+
+
+def matmul_int_workspace_size(linear: LinearInt, max_rows: int) -> int:
+    return int(lib().moe_matmul_int_workspace_size(C.byref(linear.struct), _int32("max_rows", max_rows)))
+
+
+def grouped_int_workspace_size(linear: LinearInt, max_slots: int, max_x_rows: Optional[int] = None) -> int:
+    """max_x_rows: rows of x, as many as slots unless they are by token."""
+    max_slots = _int32("max_slots", max_slots)
+    max_x_rows = max_slots if max_x_rows is None else _int32("max_x_rows", max_x_rows)
+    return int(lib().moe_grouped_int_workspace_size(C.byref(linear.struct), max_slots, max_x_rows))
+
+
+def alloc_matmul_int_workspace(linear: LinearInt, max_rows: int) -> Optional[torch.Tensor]:
+    """The workspace matmul_int needs for up to max_rows rows of any type."""
+    return _alloc_bytes(matmul_int_workspace_size(linear, max_rows), linear.w.device)
+
+
+def alloc_grouped_int_workspace(linear: LinearInt, max_slots: int, max_x_rows: Optional[int] = None):
+    """The workspace grouped_matmul_int needs for up to max_slots slots over max_x_rows rows of x."""
+    return _alloc_bytes(grouped_int_workspace_size(linear, max_slots, max_x_rows), linear.w.device)
+
+
+def matmul_int(linear: LinearInt, x: torch.Tensor, x_scale: Optional[torch.Tensor] = None,
+              residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_matmul_int: x [rows, in] -> out [rows, out] = residual + f(x w^T + bias), f gated when the
+    linear has w_up.  x is bf16, fp16 or fp32 and quantised within the call, or int8 with x_scale fp32
+    [rows].  Rows of x, residual and out may be strided; out may be residual itself."""
+    if stream is not None or _get_device() != linear.index:
+        return _on(linear.device, stream,
+                   lambda handle: _matmul_int(linear, x, x_scale, residual, out, workspace, handle))
+    return _matmul_int(linear, x, x_scale, residual, out, workspace, _raw_stream(linear.index))
+
+
+_INT_DTYPES = {**_DTYPES, torch.int8: MOE_DTYPE_I8}
+
+
+def _x_int(linear, x, x_scale):
+    """(dtype, rows, address of x_scale) of an integer product's x."""
+    dtype = _INT_DTYPES.get(x.dtype)
+    if x.dim() != 2 or x.shape[1] != linear.in_features or dtype is None or x.get_device() != linear.index:
+        _refuse("x", x, "rows", linear.in_features, "bf16, fp16, fp32 or int8", linear.device)
+    rows = x.shape[0]
+    if rows > _INT32_MAX:
+        raise ValueError(f"x has {rows} rows, more than fit 32 bits")
+    if (x_scale is not None) != (dtype == MOE_DTYPE_I8):
+        raise ValueError("x_scale goes with an int8 x")
+    if x_scale is None:
+        return dtype, rows, None
+    if (x_scale.shape != (rows,) or x_scale.dtype is not torch.float32 or not x_scale.is_contiguous()
+            or x_scale.get_device() != linear.index):
+        raise ValueError(f"x_scale must be a contiguous fp32 [{rows}] tensor on {linear.device}")
+    return dtype, rows, x_scale.data_ptr()
+
+
+def _int_workspace(workspace, linear, size):
+    if workspace is None:
+        return _alloc_bytes(size(), linear.device)
+    if workspace.device != linear.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {linear.device}")
+    return workspace
+
+
+def _matmul_int(linear, x, x_scale, residual, out, workspace, handle):
+    device, index, K, N = linear.device, linear.index, linear.in_features, linear.out_features
+    dtype, rows, scales = _x_int(linear, x, x_scale)
+    res = None
+    res_type = res_stride = 0
+    if residual is not None:
+        res_type = _DTYPES.get(residual.dtype)
+        if residual.shape != (rows, N) or residual.get_device() != index or res_type is None:
+            _refuse("residual", residual, rows, N, "bf16, fp16 or fp32", device)
+        res, res_stride = residual.data_ptr(), _strides(residual, rows, N, "residual")
+    if out is None:
+        out = torch.empty((rows, N), dtype=linear.out_dtype, device=device)
+    elif out.shape != (rows, N) or out.dtype is not linear.out_dtype or out.get_device() != index:
+        _refuse("out", out, rows, N, linear.out_dtype, device)
+    L = lib()
+    ws = _int_workspace(workspace, linear, lambda: L.moe_matmul_int_workspace_size(linear._ref, rows))
+    st = L.moe_matmul_int(linear._ref, x.data_ptr(), dtype, _strides(x, rows, K, "x"), scales, rows, res, res_type,
+                         res_stride, out.data_ptr(), _strides(out, rows, N, "out"),
+                         None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+                         handle)
+    if st:
+        raise MoeError(st, "moe_matmul_int")
+    return out
+
+
+def grouped_matmul_int(linear: LinearInt, x: torch.Tensor, plan: Plan, n_slots: int, top_k: int = 1,
+                      rows: str = "token", x_scale: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """moe_grouped_matmul_int over a plan of n_slots slots: out [n_slots, out].  x as for matmul_int, ``rows``
+    as for grouped_matmul."""
+    n_slots, top_k = int(n_slots), int(top_k)
+    if stream is not None or _get_device() != linear.index:
+        return _on(linear.device, stream, lambda handle: _grouped_int(linear, x, plan, n_slots, top_k, rows, x_scale,
+                                                                     out, workspace, handle))
+    return _grouped_int(linear, x, plan, n_slots, top_k, rows, x_scale, out, workspace, _raw_stream(linear.index))
+
+
+def _grouped_int(linear, x, plan, n_slots, top_k, rows, x_scale, out, workspace, handle):
+    device, index, K, N = linear.device, linear.index, linear.in_features, linear.out_features
+    mode = _ROWS.get(rows)
+    if mode is None:
+        raise ValueError(f"rows must be one of {sorted(_ROWS)}")
+    if not 0 <= n_slots <= _INT32_MAX or not 1 <= top_k <= _INT32_MAX:
+        raise ValueError("n_slots must be at least 0 and top_k at least 1, and both fit 32 bits")
+    dtype, x_rows, scales = _x_int(linear, x, x_scale)
+    if x_rows != (-(-n_slots // top_k) if mode == MOE_ROWS_TOKEN else n_slots):
+        raise ValueError(f"x has {x_rows} rows, which does not fit {n_slots} slots with rows={rows!r}, top_k={top_k}")
+    work, slots = plan.work, plan.sorted_slots
+    if work.numel() < 4 * min(linear.n_groups, max(n_slots, 1)) or work.get_device() != index:
+        raise ValueError(f"the plan's records are too few for {linear.n_groups} experts or not on {device}")
+    if mode != MOE_ROWS_SORTED and (slots.numel() < n_slots or slots.get_device() != index):
+        raise ValueError(f"the plan's sorted_slots are fewer than {n_slots} or not on {device}")
+    if out is None:
+        out = torch.empty((n_slots, N), dtype=linear.out_dtype, device=device)
+    elif out.shape != (n_slots, N) or out.dtype is not linear.out_dtype or out.get_device() != index:
+        _refuse("out", out, n_slots, N, linear.out_dtype, device)
+    L = lib()
+    ws = _int_workspace(workspace, linear, lambda: L.moe_grouped_int_workspace_size(linear._ref, n_slots, x_rows))
+    st = L.moe_grouped_matmul_int(linear._ref, x.data_ptr(), dtype, _strides(x, x_rows, K, "x"), scales, n_slots, top_k,
+                                 mode, C.byref(plan.struct), out.data_ptr(), _strides(out, n_slots, N, "out"),
+                                 None if ws is None else ws.data_ptr(),
+                                 0 if ws is None else ws.numel() * ws.element_size(), handle)
+    if st:
+        raise MoeError(st, "moe_grouped_matmul_int")
     return out

@@ -173,9 +173,9 @@ MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bo
     return best;  // tiles_n == 0: more workgroups than a launch takes
 }
 
-static bool linear_aligned(const moe_linear_t *L) {
+static bool linear_aligned(const moe_linear_t *L, int32_t row_tail) {
     const int64_t per = 16 / (int64_t)dtype_size(L->dtype);
-    if (L->in_features % per || !aligned(L->w, 16) || (L->w_up && !aligned(L->w_up, 16))) return false;
+    if ((L->in_features + row_tail) % per || !aligned(L->w, 16) || (L->w_up && !aligned(L->w_up, 16))) return false;
     if (stride_or(L->row_stride, L->in_features) % per) return false;
     return L->n_groups == 1 || L->group_stride % per == 0;
 }
@@ -186,6 +186,15 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
                           size_t workspace_bytes, MatmulArgs *a, MatmulChoice *choice) {
     const moe_status st = check_linear(L);
     if (st != MOE_OK) return st;
+    return prepare_product(L, (int32_t)dtype_size(L->dtype), 0, x, x_stride, rows, top_k, rows_mode, plan, residual,
+                           residual_dtype, residual_stride, out, out_stride, workspace, workspace_bytes, a, choice);
+}
+
+moe_status prepare_product(const moe_linear_t *L, int32_t bias_size, int32_t row_tail, const void *x, int64_t x_stride,
+                           int32_t rows, int32_t top_k, int32_t rows_mode, const moe_plan_t *plan,
+                           const void *residual, int32_t residual_dtype, int64_t residual_stride, void *out,
+                           int64_t out_stride, void *workspace, size_t workspace_bytes, MatmulArgs *a,
+                           MatmulChoice *choice) {
     const bool grouped = rows_mode != kRowsDense;
     a->rows = 0;
     if (rows < 0 || x_stride < 0 || out_stride < 0 || residual_stride < 0) return MOE_ERR_INVALID_ARG;
@@ -198,7 +207,7 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
     if (grouped && (!plan || !plan->work || !aligned(plan->work, 16) ||
                     (rows_mode != MOE_ROWS_SORTED && !plan->sorted_slots)))
         return MOE_ERR_INVALID_ARG;
-    const size_t es = dtype_size(L->dtype), os = dtype_size(L->out_dtype);
+    const size_t es = dtype_size(L->dtype), os = dtype_size(L->out_dtype), bs = (size_t)bias_size;
     const size_t rs = residual ? dtype_size(residual_dtype) : 1;
     if (!x || !out || !aligned(x, es) || !aligned(out, os) || (residual && !aligned(residual, rs)))
         return MOE_ERR_INVALID_ARG;
@@ -213,7 +222,7 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
     // gathered rows of x are 32-bit offsets from x in the kernels for aligned rows
     const int64_t x_rows = grouped && rows_mode == MOE_ROWS_TOKEN ? tiles(rows, top_k) : rows;
     const bool near = !grouped || rows_mode == MOE_ROWS_SORTED || x_rows * xs * (int64_t)es < (int64_t)UINT32_MAX;
-    const bool al = near && linear_aligned(L) && aligned(x, 16) && xs * (int64_t)es % 16 == 0;
+    const bool al = near && linear_aligned(L, row_tail) && aligned(x, 16) && xs * (int64_t)es % 16 == 0;
     *choice = choose_matmul(L, rows, grouped, al);
     if (choice->tiles_n == 0) return MOE_ERR_UNSUPPORTED;
 
@@ -228,9 +237,9 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
     const Span reads[5] = {{x, x_rows, L->in_features * (int64_t)es, xs * (int64_t)es},
                            {L->w, L->n_groups, mat * (int64_t)es, group * (int64_t)es},
                            {L->w_up, L->w_up ? L->n_groups : 0, mat * (int64_t)es, group * (int64_t)es},
-                           {L->bias, L->bias ? L->n_groups : 0, L->out_features * (int64_t)es, bias_group * (int64_t)es},
-                           {L->bias_up, L->bias_up ? L->n_groups : 0, L->out_features * (int64_t)es,
-                            bias_group * (int64_t)es}};
+                           {L->bias, L->bias ? L->n_groups : 0, L->out_features * (int64_t)bs, bias_group * (int64_t)bs},
+                           {L->bias_up, L->bias_up ? L->n_groups : 0, L->out_features * (int64_t)bs,
+                            bias_group * (int64_t)bs}};
     for (const Span &s : reads)
         if (spans_overlap(so, s)) return MOE_ERR_INVALID_ARG;
     const int64_t records = rows < L->n_groups ? rows : L->n_groups;
@@ -264,13 +273,13 @@ moe_status prepare_matmul(const moe_linear_t *L, const void *x, int64_t x_stride
     a->x_stride = xs * (int64_t)es;
     a->w_row = row * (int64_t)es;
     a->w_group = group * (int64_t)es;
-    a->bias_group = bias_group * (int64_t)es;
+    a->bias_group = bias_group * (int64_t)bs;
     a->res_stride = rs_row;
     a->out_stride = os_row;
     a->work = grouped ? (const int4 *)plan->work : nullptr;
     a->slots = grouped && rows_mode != MOE_ROWS_SORTED ? plan->sorted_slots : nullptr;
     a->rows = rows;
-    a->K = L->in_features;
+    a->K = L->in_features + (al ? row_tail : 0);
     a->N = L->out_features;
     a->groups = L->n_groups;
     a->top_k = grouped ? top_k : 1;
@@ -317,18 +326,10 @@ moe_status check_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx
     return MOE_OK;
 }
 
-}  // namespace moe
-
-extern "C" {
-
-moe_status moe_linear_check(const moe_linear_t *linear) { return moe::check_linear(linear); }
-
 // Enough for every batch of up to max_rows rows, whatever the alignment of x: the
 // largest workspace of each tile, as its tiles grow with the rows until they are too
 // many to split.
-static size_t matmul_workspace(const moe_linear_t *linear, int32_t max_rows, bool grouped) {
-    using namespace moe;
-    if (check_linear(linear) != MOE_OK || max_rows < 1) return 0;
+size_t product_workspace(const moe_linear_t *linear, int32_t max_rows, bool grouped) {
     const int64_t steps = tiles(linear->in_features * (int64_t)dtype_size(linear->dtype), 128);
     size_t most = 0;
     for (const Cost &k : kCosts) {
@@ -346,12 +347,20 @@ static size_t matmul_workspace(const moe_linear_t *linear, int32_t max_rows, boo
     return most;
 }
 
+}  // namespace moe
+
+extern "C" {
+
+moe_status moe_linear_check(const moe_linear_t *linear) { return moe::check_linear(linear); }
+
 size_t moe_matmul_workspace_size(const moe_linear_t *linear, int32_t max_rows) {
-    return matmul_workspace(linear, max_rows, false);
+    if (moe::check_linear(linear) != MOE_OK || max_rows < 1) return 0;
+    return moe::product_workspace(linear, max_rows, false);
 }
 
 size_t moe_grouped_workspace_size(const moe_linear_t *linear, int32_t max_slots) {
-    return matmul_workspace(linear, max_slots, true);
+    if (moe::check_linear(linear) != MOE_OK || max_slots < 1) return 0;
+    return moe::product_workspace(linear, max_slots, true);
 }
 
 }  // extern "C"

@@ -1,13 +1,14 @@
-// Device side shared by the kernels of the unquantised products
-// (moe_matmul, moe_grouped_matmul; gfx950).
+// Device side shared by the kernels of the products (moe_matmul,
+// moe_grouped_matmul and their 8-bit integer forms; gfx950).
 //
 // Operands.  Rows of x and of w are read in 16-byte chunks (8 bf16 or fp16,
-// 4 fp32), 64 bytes of a row per MFMA step: v_mfma_f32_16x16x32_{bf16,f16},
-// or four v_mfma_f32_16x16x4_f32, with the weights as the A operand and x as
+// 4 fp32, 16 8-bit integers), 64 bytes of a row per MFMA step:
+// v_mfma_f32_16x16x32_{bf16,f16}, four v_mfma_f32_16x16x4_f32 or
+// v_mfma_i32_16x16x64_i8, with the weights as the A operand and x as
 // the B operand.  Lane l holds chunk l / 16 of the step for row l % 16 of
 // either operand; which inputs the chunk holds is the same on both sides, so
 // any chunk order gives the dot product.  The products of bf16 and fp16 are
-// exact in fp32, sums are fp32.  D: lane l holds rows 4 (l / 16) + r, r = 0..3, of A
+// exact in fp32, sums are fp32; integer sums are exact in 32 bits.  D: lane l holds rows 4 (l / 16) + r, r = 0..3, of A
 // (output columns) for row l % 16 of B (a row of x).
 #pragma once
 
@@ -21,10 +22,24 @@ namespace moe {
 
 typedef __attribute__((ext_vector_type(4))) float mm_f32x4;
 typedef __attribute__((ext_vector_type(4))) uint32_t mm_u32x4;
+typedef __attribute__((ext_vector_type(4))) int32_t mm_i32x4;
 typedef __attribute__((ext_vector_type(8))) __bf16 mm_bf16x8;
 typedef __attribute__((ext_vector_type(8))) _Float16 mm_f16x8;
 
-// One 64-byte step of a 16 x 16 tile.
+// A kernel's arguments.
+template <int DT>
+struct ArgsOf {
+    typedef MatmulArgs type;
+};
+template <>
+struct ArgsOf<MOE_DTYPE_I8> {
+    typedef MatmulI8Args type;
+};
+template <int DT>
+using Args = typename ArgsOf<DT>::type;
+
+// One 64-byte step of a 16 x 16 tile.  Accumulators are mm_f32x4 for every type; those of
+// integer products hold the bits of 32-bit integers until scale_row widens them.
 template <int DT>
 __device__ __forceinline__ mm_f32x4 mma(const mm_u32x4 &a, const mm_u32x4 &b, mm_f32x4 c) {
     if constexpr (DT == MOE_DTYPE_BF16) {
@@ -33,6 +48,10 @@ __device__ __forceinline__ mm_f32x4 mma(const mm_u32x4 &a, const mm_u32x4 &b, mm
     } else if constexpr (DT == MOE_DTYPE_F16) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(mm_f16x8, a),
                                                       __builtin_bit_cast(mm_f16x8, b), c, 0, 0, 0);
+    } else if constexpr (DT == MOE_DTYPE_I8) {
+        return __builtin_bit_cast(mm_f32x4, __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                                                __builtin_bit_cast(mm_i32x4, a), __builtin_bit_cast(mm_i32x4, b),
+                                                __builtin_bit_cast(mm_i32x4, c), 0, 0, 0));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -41,8 +60,17 @@ __device__ __forceinline__ mm_f32x4 mma(const mm_u32x4 &a, const mm_u32x4 &b, mm
     }
 }
 
+// The sum of two accumulators.
 template <int DT>
-constexpr int kElemBytes = DT == MOE_DTYPE_F32 ? 4 : 2;
+__device__ __forceinline__ mm_f32x4 add_acc(const mm_f32x4 &a, const mm_f32x4 &b) {
+    if constexpr (DT == MOE_DTYPE_I8)
+        return __builtin_bit_cast(mm_f32x4, __builtin_bit_cast(mm_i32x4, a) + __builtin_bit_cast(mm_i32x4, b));
+    else
+        return a + b;
+}
+
+template <int DT>
+constexpr int kElemBytes = DT == MOE_DTYPE_F32 ? 4 : DT == MOE_DTYPE_I8 ? 1 : 2;
 template <int DT>
 constexpr int kChunk = 16 / kElemBytes<DT>;  // elements of a 16-byte chunk
 
@@ -77,6 +105,8 @@ __device__ __forceinline__ mm_u32x4 load_chunk(const char *row, int c, int K) {
                 if (i < left) {
                     if constexpr (DT == MOE_DTYPE_F32)
                         v[i] = ((const uint32_t *)(row + (int64_t)c * 16))[i];
+                    else if constexpr (DT == MOE_DTYPE_I8)
+                        v[i / 4] |= (uint32_t)((const uint8_t *)(row + (int64_t)c * 16))[i] << (8 * (i % 4));
                     else
                         v[i / 2] |= (uint32_t)((const uint16_t *)(row + (int64_t)c * 16))[i] << (16 * (i % 2));
                 }
@@ -303,7 +333,7 @@ __device__ __forceinline__ void finish_row(const MatmulArgs &a, int o, int col, 
 // The biases of a lane's columns (zero without one; -0, which changes no sum).
 // Columns from N on take the last column's; the store drops them.
 template <int DT, bool GATED, int NT>
-__device__ __forceinline__ void load_bias(const MatmulArgs &a, int group, int col, mm_f32x4 *b) {
+__device__ __forceinline__ void load_bias(const Args<DT> &a, int group, int col, mm_f32x4 *b) {
     constexpr int NC = GATED ? NT / 2 : NT;
 #pragma unroll
     for (int n = 0; n < NT; ++n) b[n] = mm_f32x4{-0.f, -0.f, -0.f, -0.f};
@@ -314,8 +344,39 @@ __device__ __forceinline__ void load_bias(const MatmulArgs &a, int group, int co
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
             const int c = col + acc_col<NC>(n % NC) + r;
-            b[n][r] = load_value(p, c < a.N ? c : a.N - 1, DT);
+            if constexpr (DT == MOE_DTYPE_I8)
+                b[n][r] = load_value(p, c < a.N ? c : a.N - 1, a.bias_dtype);
+            else
+                b[n][r] = load_value(p, c < a.N ? c : a.N - 1, DT);
         }
+    }
+}
+
+// What a lane's integer products are scaled with: a factor for each of its columns, as load_bias
+// has them, and one for the row.  A row's sum is rounded to fp32 once, the two factors'
+// product once and theirs once.  Nothing of it exists for the other types.
+template <int DT, bool GATED, int NT>
+__device__ __forceinline__ void load_scales(const Args<DT> &a, int group, int col, mm_f32x4 *sc) {
+    if constexpr (DT == MOE_DTYPE_I8) {
+        constexpr int NC = GATED ? NT / 2 : NT;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float *p = (n < NC ? a.w_scale : a.w_up_scale) + (int64_t)group * a.scale_group;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int c = col + acc_col<NC>(n % NC) + r;
+                sc[n][r] = p[c < a.N ? c : a.N - 1];
+            }
+        }
+    }
+}
+template <int DT, int NT>
+__device__ __forceinline__ void scale_row(mm_f32x4 *z, const mm_f32x4 *sc, float row) {
+    if constexpr (DT == MOE_DTYPE_I8) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) z[n][r] = (float)__float_as_int(z[n][r]) * (row * sc[n][r]);
     }
 }
 
@@ -431,6 +492,15 @@ __device__ __forceinline__ int out_row(const MatmulArgs &a, const MatmulTile &t,
 __device__ __forceinline__ int x_row(const MatmulArgs &a, int out_row) {
     if (out_row < 0) return 0;
     return a.rows_mode == MOE_ROWS_TOKEN ? out_row / a.top_k : out_row;
+}
+
+// The factor of that row of x (1 where there are none).
+template <int DT>
+__device__ __forceinline__ float x_factor(const Args<DT> &a, int out_row) {
+    if constexpr (DT == MOE_DTYPE_I8)
+        return a.x_scale[x_row(a, out_row)];
+    else
+        return 1.f;
 }
 
 }  // namespace moe

@@ -1,0 +1,195 @@
+// Host-only part of the 8-bit integer products: argument checks, the workspace's layout and
+// its sizes.  Nothing here touches the device.
+#include <stdint.h>
+
+#include "matmul_internal.h"
+
+namespace moe {
+
+static bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
+static bool float_dtype(int32_t d) { return d == MOE_DTYPE_F32 || d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
+static int64_t stride_or(int64_t stride, int64_t packed) { return stride ? stride : packed; }
+static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+constexpr int64_t kMaxRowBytes = 1 << 24;
+constexpr int64_t kMaxGroupElems = (int64_t)1 << 40;
+
+moe_status check_quantize(const void *x, int32_t dtype, int64_t x_stride, int32_t n_rows, int32_t n_cols,
+                          const int8_t *codes, int64_t codes_stride, const float *scales, QuantizeArgs *a) {
+    a->rows = 0;
+    if (n_rows < 0 || n_cols < 1 || x_stride < 0 || codes_stride < 0 || !float_dtype(dtype)) return MOE_ERR_INVALID_ARG;
+    const int64_t es = (int64_t)dtype_size(dtype);
+    const int64_t xs = stride_or(x_stride, n_cols), cs = stride_or(codes_stride, n_cols);
+    if (xs < n_cols || cs < n_cols) return MOE_ERR_INVALID_ARG;
+    if (xs >= kMaxRowBytes / es || cs >= kMaxRowBytes || n_rows > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+    if (n_rows == 0) return MOE_OK;
+    if (!x || !codes || !scales || !aligned(x, (uintptr_t)es) || !aligned(scales, 4)) return MOE_ERR_INVALID_ARG;
+    const Span sx{x, n_rows, n_cols * es, xs * es}, sc{codes, n_rows, n_cols, cs}, ss{scales, 1, (int64_t)n_rows * 4, 1};
+    if (spans_overlap(sx, sc) || spans_overlap(sx, ss) || spans_overlap(sc, ss)) return MOE_ERR_INVALID_ARG;
+    *a = QuantizeArgs{(const char *)x, (int8_t *)codes, (float *)scales, xs * es, cs, n_rows, n_cols, n_cols};
+    return MOE_OK;
+}
+
+moe_status check_linear_i8(const moe_linear_int_t *L) {
+    if (!L) return MOE_ERR_INVALID_ARG;
+    if (L->in_features < 1 || L->out_features < 1 || L->n_groups < 1) return MOE_ERR_INVALID_ARG;
+    if (L->n_groups > MOE_MAX_EXPERTS || L->in_features > MOE_MAX_I8_INPUTS) return MOE_ERR_UNSUPPORTED;
+    if (!float_dtype(L->out_dtype) || !float_dtype(L->bias_dtype)) return MOE_ERR_INVALID_ARG;
+    if (L->fn < MOE_FN_NONE || L->fn > MOE_FN_GELU_TANH) return MOE_ERR_INVALID_ARG;
+    if (!(L->clamp_limit >= 0.0f) || L->clamp_limit > 3.0e38f) return MOE_ERR_INVALID_ARG;
+    if (!L->w || !L->w_scale || !L->w_up != !L->w_up_scale) return MOE_ERR_INVALID_ARG;
+    if (!L->bias_up != !(L->bias && L->w_up)) return MOE_ERR_INVALID_ARG;
+    const size_t bs = dtype_size(L->bias_dtype);
+    if (!aligned(L->w_scale, 4) || !aligned(L->w_up_scale, 4) || !aligned(L->bias, bs) || !aligned(L->bias_up, bs))
+        return MOE_ERR_INVALID_ARG;
+    if (L->row_stride < 0 || L->group_stride < 0 || L->scale_stride < 0 || L->bias_stride < 0) return MOE_ERR_INVALID_ARG;
+    const int64_t row = stride_or(L->row_stride, L->in_features);
+    if (L->row_tail < 0 || L->row_tail > 15 || row < L->in_features + L->row_tail) return MOE_ERR_INVALID_ARG;
+    if (row >= kMaxRowBytes) return MOE_ERR_UNSUPPORTED;
+    if (L->n_groups > 1) {
+        const int64_t mat = (L->out_features - 1) * row + L->in_features + L->row_tail;
+        if (L->group_stride && L->group_stride < mat) return MOE_ERR_INVALID_ARG;
+        if (L->scale_stride && L->scale_stride < L->out_features) return MOE_ERR_INVALID_ARG;
+        if (L->bias && L->bias_stride && L->bias_stride < L->out_features) return MOE_ERR_INVALID_ARG;
+        if (stride_or(L->group_stride, L->out_features * row) > kMaxGroupElems || L->scale_stride > kMaxGroupElems ||
+            L->bias_stride > kMaxGroupElems)
+            return MOE_ERR_UNSUPPORTED;
+    }
+    return MOE_OK;
+}
+
+// The product as its kernels' choice and checks see it: operands of one byte.
+static moe_linear_t as_linear(const moe_linear_int_t *L) {
+    moe_linear_t v{};
+    v.in_features = L->in_features;
+    v.out_features = L->out_features;
+    v.n_groups = L->n_groups;
+    v.dtype = MOE_DTYPE_I8;
+    v.out_dtype = L->out_dtype;
+    v.fn = L->fn;
+    v.clamp_limit = L->clamp_limit;
+    v.w = L->w;
+    v.w_up = L->w_up;
+    v.bias = L->bias;
+    v.bias_up = L->bias_up;
+    v.row_stride = stride_or(L->row_stride, L->in_features);
+    v.group_stride = L->group_stride;
+    v.bias_stride = L->bias_stride;
+    return v;
+}
+
+// A call's rows of x as integers: codes, then their scales, then the product's own part.
+struct I8Workspace {
+    int64_t stride;
+    size_t scales, parts;
+};
+static I8Workspace i8_workspace(int64_t x_rows, int64_t in_features) {
+    I8Workspace w;
+    w.stride = (in_features + 15) / 16 * 16;
+    w.scales = align256((size_t)(x_rows * w.stride));
+    w.parts = w.scales + align256((size_t)x_rows * sizeof(float));
+    return w;
+}
+
+moe_status prepare_matmul_i8(const moe_linear_int_t *L, const void *x, int32_t x_dtype, int64_t x_stride,
+                             const float *x_scale, int32_t rows, int32_t top_k, int32_t rows_mode,
+                             const moe_plan_t *plan, const void *residual, int32_t residual_dtype,
+                             int64_t residual_stride, void *out, int64_t out_stride, void *workspace,
+                             size_t workspace_bytes, MatmulI8Args *a, MatmulChoice *choice, QuantizeArgs *quantize,
+                             void **parts) {
+    a->rows = 0;
+    quantize->rows = 0;
+    *parts = workspace;
+    moe_status st = check_linear_i8(L);
+    if (st != MOE_OK) return st;
+    const bool own = x_dtype != MOE_DTYPE_I8;  // quantised here
+    if (rows < 0 || x_stride < 0 || (own && (!float_dtype(x_dtype) || x_scale)) || (rows > 0 && (!x || (!own && !x_scale))) ||
+        !aligned(x_scale, 4))
+        return MOE_ERR_INVALID_ARG;
+    // what the quantisation below counts with; prepare_product checks them again, with the rest
+    const bool by_token = rows_mode == MOE_ROWS_TOKEN;
+    if (by_token && top_k < 1) return MOE_ERR_INVALID_ARG;
+    const int64_t x_rows = by_token ? ((int64_t)rows + top_k - 1) / top_k : rows;
+    const int64_t K = L->in_features;
+    const moe_linear_t view = as_linear(L);
+    const void *px = x;
+    int64_t px_stride = x_stride;
+    const I8Workspace w = i8_workspace(x_rows, K);
+    size_t used = 0;
+    if (own && rows > 0) {
+        if (rows > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
+        if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
+        used = w.parts;
+        if (workspace_bytes < used) return MOE_ERR_WORKSPACE;
+        px = workspace;
+        px_stride = w.stride;
+        x_scale = (const float *)((char *)workspace + w.scales);
+        *parts = (char *)workspace + used;
+        st = check_quantize(x, x_dtype, x_stride, (int32_t)x_rows, L->in_features, (int8_t *)workspace, w.stride, x_scale,
+                            quantize);
+        if (st != MOE_OK) return st;
+        quantize->codes_end = (int)w.stride;
+    }
+    // rows of w may be read to the end of their last chunk where x's own rows are
+    // padded as well
+    const int32_t tail = own || K % 16 == 0 ? L->row_tail : 0;
+    const int32_t fit = tail && (K + tail) % 16 == 0 ? tail : 0;
+    st = prepare_product(&view, (int32_t)dtype_size(L->bias_dtype), fit, px, px_stride, rows, top_k, rows_mode, plan, residual,
+                         residual_dtype, residual_stride, out, out_stride, *parts, workspace_bytes - used, a, choice);
+    if (st != MOE_OK || rows == 0) return st;
+
+    // beyond what prepare_product compares: out and the whole workspace against the scales, x as it was
+    // given, and (the integers' place) everything else
+    const int64_t N = L->out_features, G = L->n_groups;
+    const int64_t sg = stride_or(G == 1 ? 0 : L->scale_stride, N), bg = stride_or(G == 1 ? 0 : L->bias_stride, N);
+    const int64_t es = own ? (int64_t)dtype_size(x_dtype) : 1, bs = (int64_t)dtype_size(L->bias_dtype);
+    const int64_t row = view.row_stride, group = stride_or(G == 1 ? 0 : L->group_stride, N * row);
+    const int64_t mat = (N - 1) * row + K + L->row_tail;
+    const int64_t rs = residual ? (int64_t)dtype_size(residual_dtype) : 1, os = (int64_t)dtype_size(L->out_dtype);
+    const Span so{out, rows, N * os, stride_or(out_stride, N) * os};
+    const Span reads[] = {
+        {L->w_scale, G, N * 4, sg * 4},
+        {L->w_up_scale, L->w_up_scale ? G : 0, N * 4, sg * 4},
+        {x, x_rows, K * es, stride_or(x_stride, K) * es},
+        {own ? nullptr : x_scale, own ? 0 : 1, x_rows * 4, 1},
+        {L->w, G, mat, group},
+        {L->w_up, L->w_up ? G : 0, mat, group},
+        {L->bias, L->bias ? G : 0, N * bs, bg * bs},
+        {L->bias_up, L->bias_up ? G : 0, N * bs, bg * bs},
+        {residual, residual ? rows : 0, N * rs, stride_or(residual_stride, N) * rs},
+        {plan ? plan->work : nullptr, rows_mode == kRowsDense ? 0 : 1, (int64_t)(rows < G ? rows : G) * 16, 1},
+        {plan ? plan->sorted_slots : nullptr, rows_mode == kRowsDense || rows_mode == MOE_ROWS_SORTED ? 0 : 1,
+         (int64_t)rows * 4, 1}};
+    const int64_t taken = (int64_t)(used + choice->workspace);
+    const Span sw{workspace, taken ? 1 : 0, taken, 1};
+    if (spans_overlap(sw, so)) return MOE_ERR_INVALID_ARG;
+    for (const Span &s : reads)
+        if (spans_overlap(sw, s) || (&s - reads < 4 && spans_overlap(so, s))) return MOE_ERR_INVALID_ARG;
+
+    a->x_scale = x_scale;
+    a->w_scale = L->w_scale;
+    a->w_up_scale = L->w_up_scale;
+    a->scale_group = sg;
+    a->bias_dtype = L->bias_dtype;
+    return MOE_OK;
+}
+
+}  // namespace moe
+
+extern "C" {
+
+moe_status moe_linear_int_check(const moe_linear_int_t *linear) { return moe::check_linear_i8(linear); }
+
+size_t moe_matmul_int_workspace_size(const moe_linear_int_t *linear, int32_t max_rows) {
+    if (moe::check_linear_i8(linear) != MOE_OK || max_rows < 1) return 0;
+    const moe_linear_t view = moe::as_linear(linear);
+    return moe::i8_workspace(max_rows, linear->in_features).parts + moe::product_workspace(&view, max_rows, false);
+}
+
+size_t moe_grouped_int_workspace_size(const moe_linear_int_t *linear, int32_t max_slots, int32_t max_x_rows) {
+    if (moe::check_linear_i8(linear) != MOE_OK || max_slots < 1 || max_x_rows < 1) return 0;
+    const moe_linear_t view = moe::as_linear(linear);
+    return moe::i8_workspace(max_x_rows, linear->in_features).parts + moe::product_workspace(&view, max_slots, true);
+}
+
+}  // extern "C"

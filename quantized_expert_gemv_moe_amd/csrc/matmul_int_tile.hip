@@ -1,0 +1,10 @@
+// Large tiles of the 8-bit integer products: their instantiations (the kernel is in matmul_tile.h).
+#include "matmul_tile.h"
+
+namespace moe {
+
+void launch_matmul_i8_tile(const MatmulI8Args &a, const MatmulChoice &c, hipStream_t s) {
+    launch_tile_dtype<MOE_DTYPE_I8>(a, c, s);
+}
+
+}  // namespace moe

@@ -34,6 +34,14 @@ struct MatmulArgs {
     int tiles_m, tiles_n;
 };
 
+// The same for 8-bit integer operands: z = x_scale[row of x] * w_scale[column] * sum + bias.
+struct MatmulI8Args : MatmulArgs {
+    const float *x_scale;              // one for each row of x
+    const float *w_scale, *w_up_scale; // one for each column of a group, groups scale_group apart
+    int64_t scale_group;
+    int bias_dtype;                    // of bias and bias_up, either
+};
+
 // Kernels of a product.
 enum MatmulKernel {
     kMatmulAny = 0,  // 64 x 64 tile through registers, any alignment
@@ -51,7 +59,7 @@ struct MatmulChoice {
     size_t workspace;
 };
 
-inline size_t dtype_size(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+inline size_t dtype_size(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : dtype == MOE_DTYPE_I8 ? 1 : 2; }
 
 // Strided rows in device memory, for the overlap checks.
 struct Span {
@@ -68,7 +76,16 @@ moe_status prepare_matmul(const moe_linear_t *linear, const void *x, int64_t x_s
                           int32_t top_k, int32_t rows_mode, const moe_plan_t *plan, const void *residual,
                           int32_t residual_dtype, int64_t residual_stride, void *out, int64_t out_stride,
                           void *workspace, size_t workspace_bytes, MatmulArgs *args, MatmulChoice *choice);
+// The same behind the descriptor's check: biases of bias_size bytes, and row_tail elements
+// behind every row of w that are zero and may be read (with x's they fill whole chunks).
+moe_status prepare_product(const moe_linear_t *linear, int32_t bias_size, int32_t row_tail, const void *x,
+                           int64_t x_stride, int32_t rows, int32_t top_k, int32_t rows_mode, const moe_plan_t *plan,
+                           const void *residual, int32_t residual_dtype, int64_t residual_stride, void *out,
+                           int64_t out_stride, void *workspace, size_t workspace_bytes, MatmulArgs *args,
+                           MatmulChoice *choice);
 MatmulChoice choose_matmul(const moe_linear_t *linear, int64_t rows, bool grouped, bool aligned);
+// Workspace of up to max_rows rows (at least one) of a checked descriptor.
+size_t product_workspace(const moe_linear_t *linear, int32_t max_rows, bool grouped);
 moe_status check_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx, const float *topk_w,
                          int32_t n_tokens, int32_t hidden, int32_t top_k, int32_t n_experts,
                          const void *residual, int32_t residual_dtype, const void *out, int32_t out_dtype);
@@ -78,7 +95,32 @@ void launch_matmul_tile(int dtype, const MatmulArgs &args, const MatmulChoice &c
 void launch_matmul_deep(int dtype, const MatmulArgs &args, const MatmulChoice &choice, void *workspace,
                         hipStream_t stream);
 void launch_matmul_few(int dtype, const MatmulArgs &args, const MatmulChoice &choice, hipStream_t stream);
+void launch_matmul_i8_tile(const MatmulI8Args &args, const MatmulChoice &choice, hipStream_t stream);
 moe_status launch_matmul(const moe_linear_t *linear, const MatmulArgs &args, const MatmulChoice &choice,
                          void *workspace, hipStream_t stream);
+
+// --------------------------------------------------- 8-bit integer products
+// Rows to be quantised: x of a float type into codes and scales.  codes rows are
+// codes_stride bytes apart; the bytes from n_cols up to codes_end of a row are set to zero.
+struct QuantizeArgs {
+    const char *x;
+    int8_t *codes;
+    float *scales;
+    int64_t x_stride, codes_stride;  // bytes
+    int rows, cols, codes_end;
+};
+moe_status check_quantize(const void *x, int32_t dtype, int64_t x_stride, int32_t n_rows, int32_t n_cols,
+                          const int8_t *codes, int64_t codes_stride, const float *scales, QuantizeArgs *args);
+void launch_quantize(int dtype, const QuantizeArgs &args, hipStream_t stream);
+
+moe_status check_linear_i8(const moe_linear_int_t *linear);
+// Checks a call and fills the kernels' arguments.  quantize->rows > 0: x is to be quantised
+// into the workspace first.  *parts is the workspace of the product itself.
+moe_status prepare_matmul_i8(const moe_linear_int_t *linear, const void *x, int32_t x_dtype, int64_t x_stride,
+                             const float *x_scale, int32_t rows, int32_t top_k, int32_t rows_mode,
+                             const moe_plan_t *plan, const void *residual, int32_t residual_dtype,
+                             int64_t residual_stride, void *out, int64_t out_stride, void *workspace,
+                             size_t workspace_bytes, MatmulI8Args *args, MatmulChoice *choice,
+                             QuantizeArgs *quantize, void **parts);
 
 }  // namespace moe
