@@ -542,7 +542,8 @@ typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
  * A router, in host memory; bias is a device pointer.  With the logits l of a token:
  *   s = softmax(l) over all experts, or sigmoid(l)
  *   c = s + bias, in 64 bits.  Without a bias experts are in the order of l itself,
- *       in which s rises.  Scores too small for 64 bits (a sigmoid of l < -709) are zero.
+ *       in which s rises.  Scores below 1e-300 (a sigmoid of l < -690) may count
+ *       as zero.
  * An expert is masked when its logit is -infinity or the lowest finite value of the logits'
  * type, or its bias is -infinity.  The softmax leaves out experts masked by their logits.
  *   Of n_groups groups of n_experts / n_groups consecutive experts the top_groups best are

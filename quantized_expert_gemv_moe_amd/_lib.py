@@ -385,12 +385,13 @@ class Plan:
 
     @staticmethod
     def allocate(n_experts: int, max_slots: int, device="cuda") -> "Plan":
-        i32 = dict(dtype=torch.int32, device=device)
-        p = [torch.empty(n_experts, **i32), torch.empty(n_experts + 1, **i32),
-             torch.empty(max(max_slots, 1), **i32), torch.empty(n_experts, **i32), torch.empty(1, **i32),
-             torch.empty((n_experts, 4), **i32)]
-        st = PlanStruct(*[x.data_ptr() for x in p])
-        return Plan(*p, st)
+        # one buffer: work first, which has to start at 16 bytes
+        E, n = n_experts, max(max_slots, 1)
+        buf = torch.empty(7 * E + 2 + n, dtype=torch.int32, device=device)
+        work, counts, offsets, unique, n_unique, slots = buf.split_with_sizes((4 * E, E, E + 1, E, 1, n))
+        at = buf.data_ptr()
+        st = PlanStruct(at + 16 * E, at + 20 * E, at + 28 * E + 8, at + 24 * E + 4, at + 28 * E + 4, at)
+        return Plan(counts, offsets, slots, unique, n_unique, work.view(E, 4), st)
 
 
 # ------------------------------------------------------------- entry points
@@ -950,11 +951,11 @@ def _router(router, logits, plan, planned, idx, w, handle):
     if B > _INT32_MAX:
         raise ValueError(f"logits has {B} rows, more than fit 32 bits")
     if idx is None:
-        idx = torch.empty((B, k), dtype=torch.int32, device=device)
+        idx = torch.empty_strided((B, k), (k, 1), dtype=torch.int32, device=device)  # the quickest of torch's ways
     elif idx.shape != (B, k) or idx.dtype is not torch.int32 or not idx.is_contiguous() or idx.get_device() != index:
         _refuse("idx", idx, B, k, "contiguous int32", device)
     if w is None:
-        w = torch.empty((B, k), dtype=torch.float32, device=device)
+        w = torch.empty_strided((B, k), (k, 1), dtype=torch.float32, device=device)
     elif w.shape != (B, k) or w.dtype is not torch.float32 or not w.is_contiguous() or w.get_device() != index:
         _refuse("w", w, B, k, "contiguous fp32", device)
     stride = _strides(logits, B, E, "logits")

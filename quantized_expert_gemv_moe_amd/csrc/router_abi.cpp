@@ -37,7 +37,6 @@ moe_status prepare_router(const moe_router_t *r, const void *logits, int32_t dty
             return MOE_ERR_INVALID_ARG;
     }
     const int groups = r->top_groups < r->n_groups ? r->n_groups : 1;  // all kept: there is nothing to choose
-    const int per_lane = router_per_lane(r->n_experts, groups);
     *a = RouterArgs{};
     a->logits = logits;
     a->bias = r->bias;
@@ -56,8 +55,7 @@ moe_status prepare_router(const moe_router_t *r, const void *logits, int32_t dty
     a->per_group = r->n_experts / groups;
     a->top_groups = r->top_groups < groups ? r->top_groups : groups;
     a->top2 = r->group_score == MOE_GROUP_TOP2;
-    a->seg = (a->per_group + per_lane - 1) / per_lane;
-    a->lane_magic = 65536 / a->seg + 1;
+    router_lanes(a, 64);
     return MOE_OK;
 }
 

@@ -25,6 +25,37 @@ __device__ __forceinline__ uint64_t order_key(double v) {
     return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
 
+// e^x = 2^n e^r, |r| <= ln 2 / 2, by the power series to r^13, whose rest is below r^14 / 14! = 5e-18 of it.
+// 0 below -745, infinity above 709.  (Short code: what runs once comes out of the instruction cache slowly.)
+__device__ __forceinline__ double exp64(double x) {
+    x = fmin(fmax(x, -1000.0), 1000.0);
+    const double n = rint(x * 1.4426950408889634);
+    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.69314718036912382, x));
+    double p = 1.0 / 6227020800.0;
+    p = fma(p, r, 1.0 / 479001600.0);
+    p = fma(p, r, 1.0 / 39916800.0);
+    p = fma(p, r, 1.0 / 3628800.0);
+    p = fma(p, r, 1.0 / 362880.0);
+    p = fma(p, r, 1.0 / 40320.0);
+    p = fma(p, r, 1.0 / 5040.0);
+    p = fma(p, r, 1.0 / 720.0);
+    p = fma(p, r, 1.0 / 120.0);
+    p = fma(p, r, 1.0 / 24.0);
+    p = fma(p, r, 1.0 / 6.0);
+    p = fma(p, r, 0.5);
+    p = fma(p, r, 1.0);
+    p = fma(p, r, 1.0);
+    return ldexp(p, (int)n);
+}
+// 1 / d, d >= 0, by two steps of Newton's method; 0 from 1e300 on.
+__device__ __forceinline__ double rcp64(double d) {
+    double r = __builtin_amdgcn_rcp(d);
+    r = fma(fma(-d, r, 1.0), r, r);
+    r = fma(fma(-d, r, 1.0), r, r);
+    return d < 1e300 ? r : 0.0;
+}
+__device__ __forceinline__ double sigmoid64(double x) { return rcp64(1.0 + exp64(-x)); }
+
 __device__ __forceinline__ float lane_value(float v, int lane) {  // of a wave-uniform lane
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
@@ -45,6 +76,36 @@ __device__ __forceinline__ float wave_max(float v) {
     return v;
 }
 
+// A lane's PL consecutive values from v[first] on, its last one repeated past `n` of them (and none of a
+// lane without experts but the row's first).  Where every lane's values are there (`whole`, the same for the launch) they are
+// read four at a time; the type is told apart once, since loads behind branches of their own would
+// each be waited for before the next (one token of 256 experts, 16 a lane: 10.0 us so, now 6.6).
+template <int PL, int DT>
+__device__ __forceinline__ void load_lane_of(const void *v, int64_t first, int n, bool whole, float *out) {
+    if constexpr (PL >= 4) {
+        if (whole) {
+#pragma unroll
+            for (int q = 0; q < PL; q += 4) {
+                const mm_f32x4 f = load_value4(v, first + q, DT);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) out[q + i] = f[i];
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < PL; ++q) out[q] = load_value(v, first + (q < n ? q : n > 0 ? n - 1 : 0), DT);
+}
+template <int PL>
+__device__ __forceinline__ void load_lane(const void *v, int64_t first, int n, bool whole, int dtype, float *out) {
+    if (dtype == MOE_DTYPE_F32)
+        load_lane_of<PL, MOE_DTYPE_F32>(v, first, n, whole, out);
+    else if (dtype == MOE_DTYPE_BF16)
+        load_lane_of<PL, MOE_DTYPE_BF16>(v, first, n, whole, out);
+    else
+        load_lane_of<PL, MOE_DTYPE_F16>(v, first, n, whole, out);
+}
+
 // Routes token t by the calling wave.  Lane j < top_k returns the j-th expert and its weight.
 template <int PL, bool BIAS, bool GROUPS>
 __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int *id, float *weight) {
@@ -57,12 +118,13 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
 
     float l[PL];
     double b[BIAS ? PL : 1];
-    // every lane's loads are in bounds and unconditional: past its last expert it repeats one
+    const bool whole = a.per_group % PL == 0;
+    load_lane<PL>(a.logits, t * a.stride + (live ? e0 : 0), n, whole, a.dtype, l);
+    if constexpr (BIAS) {
+        float f[PL];
+        load_lane_of<PL, MOE_DTYPE_F32>(a.bias, live ? e0 : 0, n, whole, f);
 #pragma unroll
-    for (int q = 0; q < PL; ++q) {
-        const int e = q < n ? e0 + q : live ? e0 : 0;
-        l[q] = load_value(a.logits, t * a.stride + e, a.dtype);
-        if constexpr (BIAS) b[q] = (double)a.bias[e];
+        for (int q = 0; q < PL; ++q) b[q] = (double)f[q];
     }
 
     bool by_logit[PL], masked[PL], bad = false;
@@ -96,7 +158,7 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
             const bool out = q >= n || by_logit[q];
             double v = 0.0;
             if (exact)
-                v = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l[q])) : exp((double)l[q] - (double)top);
+                v = a.sigmoid ? sigmoid64((double)l[q]) : exp64((double)l[q] - (double)top);
             else
                 v = (double)expf(l[q] - top);
             v = out ? 0.0 : v;
@@ -106,7 +168,7 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
         if (!a.sigmoid) {
             total = wave_sum(total);
             if constexpr (BIAS || GROUPS) {
-                const double per = total > 0.0 ? 1.0 / total : 0.0;
+                const double per = total > 0.0 ? rcp64(total) : 0.0;
 #pragma unroll
                 for (int q = 0; q < PL; ++q) s[q] *= per;
             }
@@ -207,13 +269,282 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
     const bool mine = lane < a.top_k && !my_mask;
     if (!a.sigmoid && !all_scores) top = wave_max(mine ? my_l : -INFINITY);
     // (one pass over the wave for all of them: 64 bits cost nothing here)
-    double v = exp(a.sigmoid ? -(double)my_l : (double)my_l - (double)top);
-    v = a.sigmoid ? 1.0 / (1.0 + v) : v;
+    double v = exp64(a.sigmoid ? -(double)my_l : (double)my_l - (double)top);
+    v = a.sigmoid ? rcp64(1.0 + v) : v;
     v = mine ? v : 0.0;
     if (a.renormalise) total = wave_sum(v);
-    if (a.renormalise || !a.sigmoid) v = total > 0.0 ? v / total : 0.0;
+    if (a.renormalise || !a.sigmoid) v = total > 0.0 ? v * rcp64(total) : 0.0;
     *id = bad ? -1 : my_id;
     *weight = bad ? __uint_as_float(0x7FC00000u) : (float)(v * (double)a.scale);
+}
+
+// ------------------------------------------------- four tokens a wave
+// Sixteen lanes a token, PL experts a lane, for up to 512 experts whose groups fill whole lanes:
+// most tokens are routed by 32-bit numbers with a proof that 64 bits would not choose otherwise,
+// the others (and those with masked experts or scores that are not numbers) by the whole wave
+// as above.
+//
+// Key: where a value stands between the token's smallest and largest, in 22 bits, then 1023 - expert, so
+// that keys differ and a tie goes to the lower expert.  The mapping rises with the value, so keys
+// whose upper bits differ are in the order of the values.  Without a bias these are the logits
+// themselves: equal upper bits among the chosen are right if the logits are in order or equal.  With one the values c
+// are off by at most `delta`, and upper bits have to differ by more than twice that.  The next round's
+// largest key below m is m - 1 - min(m - 1 - key) in unsigned arithmetic, where
+// keys of m and more wrap round to the far end: three instructions for two keys, and none
+// is taken out.  One more round than top_k shows that the last choice is clear as well.  Where choices
+// are not clear, sixteen of them are put in the order of their 64-bit values (some 4 tokens of 8192); the
+// whole wave's way, for what is then still open, takes 5 us longer, as its code is cold.
+//
+// What bounds it: the instructions, some 200 a token of 256 experts.  8192 tokens of 256 experts, biased
+// and grouped: 20.2 us with a wave a token in 64 bits throughout, 7.3 so; 16384 of 128, plain:
+// 15.0 and 6.0 us.
+
+struct Max {
+    __device__ __forceinline__ float operator()(float x, float y) const { return fmaxf(x, y); }
+};
+struct Min {
+    __device__ __forceinline__ float operator()(float x, float y) const { return fminf(x, y); }
+    __device__ __forceinline__ uint32_t operator()(uint32_t x, uint32_t y) const { return x < y ? x : y; }
+};
+struct Add {
+    __device__ __forceinline__ float operator()(float x, float y) const { return x + y; }
+};
+template <int CTRL, class T>
+__device__ __forceinline__ T row_move(T v) {  // within the 16 lanes of a row
+    return __builtin_bit_cast(T, dpp32<CTRL>(__builtin_bit_cast(uint32_t, v)));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140, kShl1 = 0x101;
+template <class T, class F>
+__device__ __forceinline__ T row_reduce(T v, F f) {  // the same in all 16 lanes
+    v = f(v, row_move<kXor1>(v));
+    v = f(v, row_move<kXor2>(v));
+    v = f(v, row_move<kHalfMirror>(v));
+    return f(v, row_move<kMirror>(v));
+}
+template <int CTRL>
+__device__ __forceinline__ double row_move64(double v) {
+    return __hiloint2double((int)dpp32<CTRL>((uint32_t)__double2hiint(v)), (int)dpp32<CTRL>((uint32_t)__double2loint(v)));
+}
+__device__ __forceinline__ double row_sum(double v) {
+    v += row_move64<kXor1>(v);
+    v += row_move64<kXor2>(v);
+    v += row_move64<kHalfMirror>(v);
+    return v + row_move64<kMirror>(v);
+}
+
+// Routes tokens t0 .. t0 + 3 (those below n_tokens) by the calling wave.  Lane 16 i + j returns token
+// t0 + i's j-th expert and its weight, for j < top_k; the result is valid where the token exists.
+// a.per_group is a multiple of PL, a group's lanes a power of two.
+template <int PL, int SLOW, bool BIAS, bool GROUPS>
+__device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArgs &one, int64_t t0, int *id, float *weight) {
+    const int lane = threadIdx.x & (kWave - 1), r = lane & 15, row0 = lane & 48;
+    const int64_t t = t0 + (lane >> 4) < a.n_tokens ? t0 + (lane >> 4) : a.n_tokens - 1;
+    const bool live = r * PL < a.n_experts;
+    const int e0 = live ? r * PL : 0;  // lanes without experts repeat the first ones and leave them out of the choice
+    constexpr float kNone = -INFINITY;
+
+    float l[PL], c[PL];  // logits, and what the order goes by
+    const int64_t at = t * a.stride;
+    load_lane<PL>(a.logits, at + e0, PL, true, a.dtype, l);
+    if constexpr (BIAS) load_lane_of<PL, MOE_DTYPE_F32>(a.bias, e0, PL, true, c);
+    float l_min = l[0];
+#pragma unroll
+    for (int q = 1; q < PL; ++q) l_min = fminf(l_min, l[q]);
+    bool clear = l_min > a.lowest;
+    // scores in 32 bits
+    float top = kNone, largest = 1.f;
+    double sum = 0.0;  // of a softmax that is not renormalised
+    const bool scores = BIAS || (GROUPS && a.top2);
+    float s[(BIAS || GROUPS) ? PL : 1];
+    if (!a.sigmoid && (scores || !a.renormalise)) {
+#pragma unroll
+        for (int q = 0; q < PL; ++q) top = fmaxf(top, l[q]);
+        top = row_reduce(top, Max{});
+        float total = 0.f;
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+            const float e = expf(l[q] - top);
+            if constexpr (BIAS || GROUPS) s[q] = e;
+            total += e;
+            if (!a.renormalise) sum += (double)e;
+        }
+        if (!a.renormalise) sum = row_sum(live ? sum : 0.0);
+        largest = __builtin_amdgcn_rcpf(row_reduce(live ? total : 0.f, Add{}));
+        if constexpr (BIAS || GROUPS) {
+#pragma unroll
+            for (int q = 0; q < PL; ++q) s[q] *= largest;
+        }
+    } else if (scores) {
+        if constexpr (BIAS || GROUPS) {
+#pragma unroll
+            for (int q = 0; q < PL; ++q) s[q] = sigmoid_mul(1.0f, l[q]);
+        }
+    }
+    float lo = INFINITY, hi = kNone, zero = 0.f;  // zero becomes NaN with any value that is not finite
+#pragma unroll
+    for (int q = 0; q < PL; ++q) {
+        if constexpr (BIAS)
+            c[q] += s[q];
+        else
+            c[q] = l[q];
+        lo = fminf(lo, c[q]);
+        hi = fmaxf(hi, c[q]);
+        zero = fmaf(c[q], 0.f, zero);
+    }
+    lo = row_reduce(lo, Min{});
+    hi = row_reduce(hi, Max{});
+    clear = clear & (zero == 0.f);
+    // A sigmoid is off by at most 2.4e-7: its argument's product by |l| 2^-23, where s (1 - s) |l| < 0.23, its
+    // exponential, sum and reciprocal by 1.5 steps.  A softmax score by 1.2e-6 of the largest: the same for the
+    // exponentials, whose arguments' weighted mean is below ln 512.  And c by its addition's rounding, 2^-24 of it.
+    const float delta = (a.sigmoid ? 0x1p-21f : 0x1p-18f * largest) + 0x1p-23f * fmaxf(fabsf(lo), fabsf(hi));
+
+    bool kept = live;
+    if constexpr (GROUPS) {
+        float best = kNone, second = kNone;
+        auto add = [&](float v) {  // of three numbers in order best >= second, and v
+            second = __builtin_amdgcn_fmed3f(best, second, v);
+            best = fmaxf(best, v);
+        };
+#pragma unroll
+        for (int q = 0; q < PL; ++q) {
+            if constexpr (BIAS)
+                add(c[q]);
+            else
+                add(a.top2 ? s[q] : l[q]);
+        }
+        auto meet = [&](auto ctrl) {
+            constexpr int C = decltype(ctrl)::value;
+            const float ob = row_move<C>(best), os = row_move<C>(second);
+            second = fmaxf(fmaxf(second, os), fminf(best, ob));
+            best = fmaxf(best, ob);
+        };
+        if (a.seg >= 2) meet(Index<kXor1>{});
+        if (a.seg >= 4) meet(Index<kXor2>{});
+        if (a.seg >= 8) meet(Index<kHalfMirror>{});
+        const float mine = !live ? kNone : a.top2 && a.per_group > 1 ? best + second : best;
+        const float over = !scores ? mine : mine + 4.f * delta, under = !scores ? mine : mine - 4.f * delta;
+        // lanes whose group is surely, or maybe, before this one's; without margins lanes of equal
+        // groups to the left as well
+        int surely = 0, maybe = 0;
+        static_for<15>([&](auto i) {
+            constexpr int kRor = 0x121 + decltype(i)::value;  // row_ror: lane r takes lane (r - i - 1) & 15
+            const float other = row_move<kRor>(mine);
+            surely += other > over;
+            maybe += other > under;
+        });
+        if (!scores) {
+            const int group = (r * a.lane_magic) >> 16;
+            static_for<15>([&](auto i) {
+                constexpr int N = decltype(i)::value + 1;
+                const bool tie = row_move<0x120 + N>(mine) == mine && ((((r - N) & 15) * a.lane_magic) >> 16) < group;
+                surely += tie;
+            });
+            maybe = surely;
+        } else {
+            maybe -= a.seg - 1;  // its own
+        }
+        kept = live & (surely < a.top_groups * a.seg);
+        clear = clear & (!kept | (maybe < a.top_groups * a.seg));
+    }
+
+    constexpr uint32_t kSteps = (1u << 22) - 8;
+    float scale = (float)kSteps / (hi - lo);
+    scale = scale < 1e30f ? scale : 0.f;  // all alike (or not numbers): the check below has the last word
+    // experts out of the choice have 0 above their number, the others 1 and more
+    const float by = kept ? scale : 0.f, from = kept ? 1.5f : 0.f;
+    uint32_t key[PL];
+#pragma unroll
+    for (int q = 0; q < PL; ++q)
+        key[q] = ((uint32_t)fmaf(c[q] - lo, by, from) << 10) + (uint32_t)(1023 - r * PL) - q;
+    const int all = a.top_groups * a.per_group;
+    const bool chosen = r < a.top_k;
+    uint32_t m = 0, my_key = 0;  // lane j has the j-th choice, the last one is m
+    int j = 0;
+    auto choose = [&](int upto) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (; j < upto; ++j) {
+            const uint32_t below = m - 1u;  // round 0: every key is below
+            uint32_t d = 0xFFFFFFFFu;
+#pragma unroll
+            for (int q = 0; q < PL; ++q) d = min(d, below - key[q]);
+            m = below - row_reduce(d, Min{});
+            my_key = r == j ? m : my_key;
+        }
+    };
+    auto expert = [&](uint32_t k) {
+        const int e = 1023 - (int)(k & 1023u);
+        return e < a.n_experts ? e : 0;
+    };
+    const int rounds = a.top_k < all ? a.top_k + 1 : a.top_k;
+    choose(rounds);
+    // every choice against the next one.  Keys' gaps are right to within two of their steps.
+    const float far = BIAS ? 2.f * delta * scale + 2.f : 0.f;
+    uint32_t next = row_move<kShl1>(my_key);  // lane j takes lane j + 1's
+    next = r == a.top_k - 1 ? m : next;
+    const bool pair = chosen & (r < a.top_k - 1 || rounds > a.top_k);
+    int e = chosen ? expert(my_key) : 0;
+    float my_l;
+    load_lane<1>(a.logits, at + e, 1, false, a.dtype, &my_l);
+    bool gaps;
+    const uint32_t gap = (my_key >> 10) - (next >> 10);
+    if constexpr (BIAS) {
+        gaps = !pair | ((float)gap > far);
+    } else {
+        float l_next;
+        load_lane<1>(a.logits, at + (pair ? expert(next) : e), 1, false, a.dtype, &l_next);
+        // (what stands behind the last one looked at may have its place too)
+        gaps = !pair | (gap > 0) | ((my_l >= l_next) & (r < a.top_k - 1));
+    }
+    if (__ballot(!gaps & clear)) {
+        // Up to sixteen candidates in the order of their exact values: right if what was not looked at is
+        // clearly less than the last one chosen.
+        const int total = all < 16 ? all : 16;
+        choose(total);
+        e = r < total ? expert(my_key) : 0;
+        load_lane<1>(a.logits, at + e, 1, false, a.dtype, &my_l);
+        double exact = (double)my_l;
+        if constexpr (BIAS) exact = sigmoid64(exact) + (double)a.bias[e];
+        if (r >= total) exact = kNone;
+        int before = 0;
+        static_for<15>([&](auto i) __attribute__((always_inline)) {
+            constexpr int kRor = 0x121 + decltype(i)::value;
+            const double other = row_move64<kRor>(exact);
+            before += (other > exact) | ((other == exact) & (row_move<kRor>(e) < e));
+        });
+        before = r < total ? before : r;
+        const int to = (row0 + before) * 4;
+        e = __builtin_amdgcn_ds_permute(to, e);
+        my_l = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(my_l)));
+        const uint32_t placed = (uint32_t)__builtin_amdgcn_ds_permute(to, (int)my_key);
+        gaps = (!BIAS || a.sigmoid) &
+               ((r != a.top_k - 1) | (total == all) | (((float)((placed >> 10) - (m >> 10)) > far) & (a.top_k < total)));
+    }
+    clear = clear & gaps;
+
+    if (!a.sigmoid && a.renormalise && !scores) top = row_reduce(chosen ? my_l : kNone, Max{});
+    double v = exp64(a.sigmoid ? -(double)my_l : (double)my_l - (double)top);
+    if (a.sigmoid) v = rcp64(1.0 + v);
+    v = chosen ? v : 0.0;
+    if (a.renormalise) sum = row_sum(v);
+    if (a.renormalise || !a.sigmoid) v = sum > 0.0 ? v * rcp64(sum) : 0.0;
+    *id = e;
+    *weight = (float)(v * (double)a.scale);
+
+    unsigned long long unclear = __ballot(!clear);
+    while (unclear) {
+        const int row = __builtin_ctzll(unclear) & 48;
+        unclear &= ~(0xFFFFull << row);
+        int slow_id;
+        float slow_w;
+        const int64_t slow_t = t0 + (row >> 4);
+        if (slow_t >= a.n_tokens) break;  // rows past the end repeat the last token
+        router_token<SLOW, BIAS, GROUPS>(one, slow_t, &slow_id, &slow_w);
+        slow_id = __shfl(slow_id, r, kWave);
+        slow_w = __shfl(slow_w, r, kWave);
+        *id = row0 == row ? slow_id : *id;
+        *weight = row0 == row ? slow_w : *weight;
+    }
 }
 
 }  // namespace moe

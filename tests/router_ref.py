@@ -3,10 +3,11 @@ evaluation in fp32 and fp64 with one rounding may be from its weights.
 
 Ids are whole numbers and have to be equal.  Weights: the chosen scores, their sum and the quotient in 64
 bits, then one rounding to fp32: half a step, 2^-24 of the value (and half the smallest
-subnormal).  Softmax weights that are not renormalised and of whose experts neither a bias nor sums
-decide may take the sum over all experts from fp32 exponentials: each is off by half a step of
-its argument d = l - max (relative |d| 2^-24, as exp' = exp) and by at most two steps of its own (2^-22), so the sum
-is off by at most sum e^d (|d| 2^-24 + 2^-22) / sum e^d.
+subnormal).  Exponentials, sums and reciprocals in 64 bits are good to a few steps,
+2^-48 together.  Softmax weights that are not renormalised may take the sum over all experts (added up in 64
+bits) from fp32 exponentials: each is off by half a step of its argument d = l - max (relative
+|d| 2^-24, as exp' = exp) and by at most two steps of its own (2^-22), so the sum is off by at most
+sum e^d (|d| 2^-24 + 2^-22) / sum e^d.
 """
 
 import math
@@ -64,11 +65,11 @@ def route(logits, dtype, top_k, score, bias=None, n_groups=1, top_groups=1, by="
         pool.sort(key=lambda e: (masked[e], 0.0 if masked[e] else -order_by[e], e))
         chosen = pool[:top_k]
         v = [0.0 if masked[e] else s[e] for e in chosen]
-        off = 2.0 ** -50
+        off = 2.0 ** -48
         if renormalise:
             total = math.fsum(v)
             v = [x / total if total else 0.0 for x in v]
-        elif score == "softmax" and bias is None and not (top_groups < n_groups and by == "top2"):
+        elif score == "softmax":
             off += sum(x * (abs(y - top) * 2.0 ** -24 + 2.0 ** -22) for x, y, m in zip(s, l, by_logit) if not m)
         ids[t] = chosen
         w[t] = [x * scale for x in v]

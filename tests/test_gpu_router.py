@@ -74,6 +74,35 @@ def test_many_tokens_keep_the_exact_order():
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True], ids=["plain", "biased"])
+def test_clusters_of_close_values(score, biased):
+    """Values closer than 32 bits or a 22-bit place in their range can tell apart: a few among the
+    chosen, at the border, more than are looked at again, groups next to one another, and one far
+    value that widens the range."""
+    log(f"[case] router clusters {score} biased={biased}")
+    for E, G, keep in ((256, 1, 1), (256, 8, 4), (64, 1, 1), (512, 16, 3), (40, 1, 1), (16, 1, 1)):
+        rng = np.random.default_rng(E + G)
+        rows = []
+        for size in (2, 3, 8, 9, 12, 20, E):
+            for step in (2.0 ** -23, 2.0 ** -21, 1e-5):
+                v = rng.standard_normal(E) * 0.3
+                at = rng.permutation(E)[:min(size, E)]
+                v[at] = 1.0 + step * rng.permutation(at.size)
+                rows.append(v)
+                far = v.copy()
+                far[rng.integers(E)] = rng.choice([1e4, -1e4])
+                rows.append(far)
+        one = rng.standard_normal(E // G)
+        rows += [np.tile(one, G) + 1e-7 * rng.standard_normal(E), np.tile(one, G)]
+        logits = torch.tensor(np.array(rows), dtype=torch.float32, device="cuda")
+        bias = torch.tensor((rng.integers(0, 3, E) - 1) * 2.0 ** -20, dtype=torch.float32, device="cuda") if biased else None
+        for by in ("max", "top2"):
+            for k in (2, 8, 15, 16):
+                r = moe.Router(E, k, score=score, bias=bias, n_groups=G, top_groups=keep, group_score=by)
+                compare(logits, "fp32", r, f"clusters {E} {G} {by} k={k}")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "biased"])
 def test_ties_go_to_the_lower_expert_and_group(score, biased):
     log(f"[case] router ties {score} biased={biased}")
     for E, G, keep in ((64, 1, 1), (256, 8, 3), (160, 8, 2), (1020, 5, 2)):
