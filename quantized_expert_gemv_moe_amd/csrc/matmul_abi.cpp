@@ -173,7 +173,7 @@ MatmulChoice choose_matmul(const moe_linear_t *L, int64_t rows, bool grouped, bo
     return best;  // tiles_n == 0: more workgroups than a launch takes
 }
 
-static bool linear_aligned(const moe_linear_t *L, int32_t row_tail) {
+bool linear_aligned(const moe_linear_t *L, int32_t row_tail) {
     const int64_t per = 16 / (int64_t)dtype_size(L->dtype);
     if ((L->in_features + row_tail) % per || !aligned(L->w, 16) || (L->w_up && !aligned(L->w_up, 16))) return false;
     if (stride_or(L->row_stride, L->in_features) % per) return false;

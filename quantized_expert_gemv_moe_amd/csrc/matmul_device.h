@@ -33,7 +33,7 @@ struct ArgsOf {
 };
 template <>
 struct ArgsOf<MOE_DTYPE_I8> {
-    typedef MatmulI8Args type;
+    typedef MatmulIntArgs type;
 };
 template <int DT>
 using Args = typename ArgsOf<DT>::type;

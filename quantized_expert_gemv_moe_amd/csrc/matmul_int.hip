@@ -11,11 +11,12 @@
 
 namespace moe {
 
-static moe_status launch_i8(const MatmulI8Args &a, const MatmulChoice &c, const QuantizeArgs &q, int x_dtype,
+static moe_status launch_int(const MatmulIntFewArgs &a, const MatmulChoice &c, const QuantizeArgs &q, int x_dtype,
                             void *parts, hipStream_t s) {
     if (q.rows > 0) launch_quantize(x_dtype, q, s);
     switch (c.kernel) {
-        case kMatmulTile: launch_matmul_i8_tile(a, c, s); break;
+        case kMatmulIntFew: launch_matmul_int_few(x_dtype, a, c, s); break;
+        case kMatmulTile: launch_matmul_int_tile(a, c, s); break;
         case kMatmulDeep: launch_deep_dtype<MOE_DTYPE_I8>(a, c, parts, s); break;
         case kMatmulFew: launch_few_dtype<MOE_DTYPE_I8>(a, c, s); break;
         default: launch_any_dtype<MOE_DTYPE_I8>(a, c, s); break;
@@ -31,15 +32,15 @@ extern "C" moe_status moe_matmul_int(const moe_linear_int_t *linear, const void 
                                     const float *x_scale, int32_t n_rows, const void *residual,
                                     int32_t residual_dtype, int64_t residual_stride, void *out, int64_t out_stride,
                                     void *workspace, size_t workspace_bytes, void *hip_stream) {
-    MatmulI8Args a;
+    MatmulIntFewArgs a;
     MatmulChoice c;
     QuantizeArgs q;
     void *parts;
-    const moe_status st = prepare_matmul_i8(linear, x, x_dtype, x_stride, x_scale, n_rows, 1, kRowsDense, nullptr,
+    const moe_status st = prepare_matmul_int(linear, x, x_dtype, x_stride, x_scale, n_rows, 1, kRowsDense, nullptr,
                                             residual, residual_dtype, residual_stride, out, out_stride, workspace,
                                             workspace_bytes, &a, &c, &q, &parts);
     if (st != MOE_OK || a.rows == 0) return st;
-    return launch_i8(a, c, q, x_dtype, parts, (hipStream_t)hip_stream);
+    return launch_int(a, c, q, x_dtype, parts, (hipStream_t)hip_stream);
 }
 
 extern "C" moe_status moe_grouped_matmul_int(const moe_linear_int_t *linear, const void *x, int32_t x_dtype,
@@ -47,13 +48,13 @@ extern "C" moe_status moe_grouped_matmul_int(const moe_linear_int_t *linear, con
                                             int32_t rows, const moe_plan_t *plan, void *out, int64_t out_stride,
                                             void *workspace, size_t workspace_bytes, void *hip_stream) {
     if (rows < MOE_ROWS_TOKEN || rows > MOE_ROWS_SORTED) return MOE_ERR_INVALID_ARG;
-    MatmulI8Args a;
+    MatmulIntFewArgs a;
     MatmulChoice c;
     QuantizeArgs q;
     void *parts;
     const moe_status st =
-        prepare_matmul_i8(linear, x, x_dtype, x_stride, x_scale, n_slots, top_k, rows, plan, nullptr, 0, 0, out,
+        prepare_matmul_int(linear, x, x_dtype, x_stride, x_scale, n_slots, top_k, rows, plan, nullptr, 0, 0, out,
                           out_stride, workspace, workspace_bytes, &a, &c, &q, &parts);
     if (st != MOE_OK || a.rows == 0) return st;
-    return launch_i8(a, c, q, x_dtype, parts, (hipStream_t)hip_stream);
+    return launch_int(a, c, q, x_dtype, parts, (hipStream_t)hip_stream);
 }

@@ -9,6 +9,7 @@ namespace moe {
 static bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p % a) == 0; }
 static bool float_dtype(int32_t d) { return d == MOE_DTYPE_F32 || d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
 static int64_t stride_or(int64_t stride, int64_t packed) { return stride ? stride : packed; }
+static int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 constexpr int64_t kMaxRowBytes = 1 << 24;
@@ -30,7 +31,7 @@ moe_status check_quantize(const void *x, int32_t dtype, int64_t x_stride, int32_
     return MOE_OK;
 }
 
-moe_status check_linear_i8(const moe_linear_int_t *L) {
+moe_status check_linear_int(const moe_linear_int_t *L) {
     if (!L) return MOE_ERR_INVALID_ARG;
     if (L->in_features < 1 || L->out_features < 1 || L->n_groups < 1) return MOE_ERR_INVALID_ARG;
     if (L->n_groups > MOE_MAX_EXPERTS || L->in_features > MOE_MAX_I8_INPUTS) return MOE_ERR_UNSUPPORTED;
@@ -79,28 +80,67 @@ static moe_linear_t as_linear(const moe_linear_int_t *L) {
 }
 
 // A call's rows of x as integers: codes, then their scales, then the product's own part.
-struct I8Workspace {
+struct IntWorkspace {
     int64_t stride;
     size_t scales, parts;
 };
-static I8Workspace i8_workspace(int64_t x_rows, int64_t in_features) {
-    I8Workspace w;
+static IntWorkspace int_workspace(int64_t x_rows, int64_t in_features) {
+    IntWorkspace w;
     w.stride = (in_features + 15) / 16 * 16;
     w.scales = align256((size_t)(x_rows * w.stride));
     w.parts = w.scales + align256((size_t)x_rows * sizeof(float));
     return w;
 }
 
-moe_status prepare_matmul_i8(const moe_linear_int_t *L, const void *x, int32_t x_dtype, int64_t x_stride,
+// Whether a call takes the kernel for few rows, which quantises x by itself: a launch less than the
+// others, which cost 9.1 us and more from calls in a row (integers beforehand take one launch anyway, and
+// those), for the price that every workgroup quantises its rows again.  us of a call, two launches and one:
+//   dense     1 row, 2048 -> 768 gated    9.2  6.4    16 rows 9.1  8.2    64 rows 9.5  8.8    128 rows 9.5 10.6
+//             32 rows, 768 -> 2048        9.3  6.7    1 row, 4096 -> 4096 9.2  6.5    32 rows, 2048 -> 8192 9.7 10.8
+//             77 rows, 1003 -> 1357       9.2  7.7
+//   top-8 of 128, 2048 -> 768 gated       1 token 11.0  9.1   2 tokens 14.1 12.6   4 tokens 21.5 24.3
+//   top-8 of 128, 768 -> 2048             1 token  9.6  6.7   4 tokens 17.0 15.9   8 tokens 23.6 24.7
+//   top-2 of 8, 1024 -> 2048              1 token  9.1  6.8  32 tokens 10.7  8.1  64 tokens 10.8 11.5
+static bool choose_int_few(const moe_linear_int_t *L, const MatmulIntFewArgs &a, bool grouped, MatmulChoice *c) {
+    const int64_t K = L->in_features, units = (K + 127) / 128, columns = L->w_up ? 8 : 16;
+    const int64_t used = a.rows < L->n_groups ? a.rows : L->n_groups;
+    const int64_t tiles_m = grouped ? (a.rows + used * 15) / 16 : (a.rows + 15) / 16;
+    // a row has a chunk at least; two workgroups a CU fit its LDS
+    if (K < 16 || tiles_m > 256 || a.lds_rows * (int64_t)a.lds_stride > 56 * 1024) return false;
+    int cs = 0;
+    int64_t tiles_n = 0;
+    if (grouped) {
+        if (a.n_records > kIntFewRecords) return false;
+        cs = 4;
+        tiles_n = tiles(L->out_features, columns * cs);
+        // more rows to a tile cost more than the launch
+        if (tiles_m * tiles_n > (units <= 8 ? 1024 : 512) || a.rows > 8 * tiles_m) return false;
+    } else {
+        // the fewest columns whose workgroups have a CU each
+        for (cs = 1; cs <= 4; cs *= 2) {
+            tiles_n = tiles(L->out_features, columns * cs);
+            if (tiles_m * tiles_n <= 256) break;
+        }
+        if (cs > 4) return false;
+        // the start and end of a workgroup, the quantisation of its rows, and the loads of its
+        // weights past the first four units of a wave
+        const int64_t rows = a.rows < 16 ? a.rows : 16, batches = tiles(units * cs, 32);
+        if (4.9 + 0.1 * (double)rows * (double)K / 1024 + 1.9 * (double)(batches - 1) > 9.0) return false;
+    }
+    *c = MatmulChoice{kMatmulIntFew, 1, cs, true, (int)tiles_m, (int)tiles_n, 1, 0};
+    return true;
+}
+
+moe_status prepare_matmul_int(const moe_linear_int_t *L, const void *x, int32_t x_dtype, int64_t x_stride,
                              const float *x_scale, int32_t rows, int32_t top_k, int32_t rows_mode,
                              const moe_plan_t *plan, const void *residual, int32_t residual_dtype,
                              int64_t residual_stride, void *out, int64_t out_stride, void *workspace,
-                             size_t workspace_bytes, MatmulI8Args *a, MatmulChoice *choice, QuantizeArgs *quantize,
+                             size_t workspace_bytes, MatmulIntFewArgs *a, MatmulChoice *choice, QuantizeArgs *quantize,
                              void **parts) {
     a->rows = 0;
     quantize->rows = 0;
     *parts = workspace;
-    moe_status st = check_linear_i8(L);
+    moe_status st = check_linear_int(L);
     if (st != MOE_OK) return st;
     const bool own = x_dtype != MOE_DTYPE_I8;  // quantised here
     if (rows < 0 || x_stride < 0 || (own && (!float_dtype(x_dtype) || x_scale)) || (rows > 0 && (!x || (!own && !x_scale))) ||
@@ -114,7 +154,7 @@ moe_status prepare_matmul_i8(const moe_linear_int_t *L, const void *x, int32_t x
     const moe_linear_t view = as_linear(L);
     const void *px = x;
     int64_t px_stride = x_stride;
-    const I8Workspace w = i8_workspace(x_rows, K);
+    const IntWorkspace w = int_workspace(x_rows, K);
     size_t used = 0;
     if (own && rows > 0) {
         if (rows > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
@@ -166,6 +206,18 @@ moe_status prepare_matmul_i8(const moe_linear_int_t *L, const void *x, int32_t x
     for (const Span &s : reads)
         if (spans_overlap(sw, s) || (&s - reads < 4 && spans_overlap(so, s))) return MOE_ERR_INVALID_ARG;
 
+    a->x_in = (const char *)x;
+    a->x_in_stride = stride_or(x_stride, K) * es;
+    a->x_cols = L->in_features;
+    a->x_rows = (int)x_rows;
+    a->lds_stride = (int)((K + 127) / 128 * 128 + 16);
+    a->lds_rows = rows_mode == kRowsDense && rows < 16 ? rows : 16;
+    if (own && linear_aligned(&view, L->row_tail) && choose_int_few(L, *a, rows_mode != kRowsDense, choice)) {
+        a->K = (int)K + L->row_tail;  // x's rows are padded with zeros in LDS
+        a->tiles_m = choice->tiles_m;
+        a->tiles_n = choice->tiles_n;
+        quantize->rows = 0;
+    }
     a->x_scale = x_scale;
     a->w_scale = L->w_scale;
     a->w_up_scale = L->w_up_scale;
@@ -178,18 +230,18 @@ moe_status prepare_matmul_i8(const moe_linear_int_t *L, const void *x, int32_t x
 
 extern "C" {
 
-moe_status moe_linear_int_check(const moe_linear_int_t *linear) { return moe::check_linear_i8(linear); }
+moe_status moe_linear_int_check(const moe_linear_int_t *linear) { return moe::check_linear_int(linear); }
 
 size_t moe_matmul_int_workspace_size(const moe_linear_int_t *linear, int32_t max_rows) {
-    if (moe::check_linear_i8(linear) != MOE_OK || max_rows < 1) return 0;
+    if (moe::check_linear_int(linear) != MOE_OK || max_rows < 1) return 0;
     const moe_linear_t view = moe::as_linear(linear);
-    return moe::i8_workspace(max_rows, linear->in_features).parts + moe::product_workspace(&view, max_rows, false);
+    return moe::int_workspace(max_rows, linear->in_features).parts + moe::product_workspace(&view, max_rows, false);
 }
 
 size_t moe_grouped_int_workspace_size(const moe_linear_int_t *linear, int32_t max_slots, int32_t max_x_rows) {
-    if (moe::check_linear_i8(linear) != MOE_OK || max_slots < 1 || max_x_rows < 1) return 0;
+    if (moe::check_linear_int(linear) != MOE_OK || max_slots < 1 || max_x_rows < 1) return 0;
     const moe_linear_t view = moe::as_linear(linear);
-    return moe::i8_workspace(max_x_rows, linear->in_features).parts + moe::product_workspace(&view, max_slots, true);
+    return moe::int_workspace(max_x_rows, linear->in_features).parts + moe::product_workspace(&view, max_slots, true);
 }
 
 }  // extern "C"

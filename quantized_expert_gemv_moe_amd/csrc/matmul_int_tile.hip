@@ -3,7 +3,7 @@
 
 namespace moe {
 
-void launch_matmul_i8_tile(const MatmulI8Args &a, const MatmulChoice &c, hipStream_t s) {
+void launch_matmul_int_tile(const MatmulIntArgs &a, const MatmulChoice &c, hipStream_t s) {
     launch_tile_dtype<MOE_DTYPE_I8>(a, c, s);
 }
 

@@ -35,11 +35,21 @@ struct MatmulArgs {
 };
 
 // The same for 8-bit integer operands: z = x_scale[row of x] * w_scale[column] * sum + bias.
-struct MatmulI8Args : MatmulArgs {
+struct MatmulIntArgs : MatmulArgs {
     const float *x_scale;              // one for each row of x
     const float *w_scale, *w_up_scale; // one for each column of a group, groups scale_group apart
     int64_t scale_group;
     int bias_dtype;                    // of bias and bias_up, either
+};
+
+// The kernel for few rows of an integer product, which takes x as it is given and finds its tile among up to so
+// many records.
+constexpr int kIntFewRecords = 256;
+struct MatmulIntFewArgs : MatmulIntArgs {
+    const char *x_in;
+    int64_t x_in_stride;             // bytes
+    int x_cols, x_rows;              // in_features (K may count the zeros behind them); rows of x
+    int lds_rows, lds_stride;        // rows of x in LDS, bytes apart
 };
 
 // Kernels of a product.
@@ -48,6 +58,7 @@ enum MatmulKernel {
     kMatmulTile,     // large tile straight into LDS, aligned rows
     kMatmulDeep,     // small tile, many stages of LDS, aligned rows
     kMatmulFew,      // few rows: w straight into registers, K split over waves
+    kMatmulIntFew,   // the same for integer products, dense or grouped, x quantised in the kernel; nt: groups of 16 (gated 8) columns
 };
 
 struct MatmulChoice {
@@ -84,6 +95,8 @@ moe_status prepare_product(const moe_linear_t *linear, int32_t bias_size, int32_
                            int64_t out_stride, void *workspace, size_t workspace_bytes, MatmulArgs *args,
                            MatmulChoice *choice);
 MatmulChoice choose_matmul(const moe_linear_t *linear, int64_t rows, bool grouped, bool aligned);
+// Whether the rows of the weights, with row_tail elements behind each, are whole chunks at 16-byte addresses.
+bool linear_aligned(const moe_linear_t *linear, int32_t row_tail);
 // Workspace of up to max_rows rows (at least one) of a checked descriptor.
 size_t product_workspace(const moe_linear_t *linear, int32_t max_rows, bool grouped);
 moe_status check_combine(const void *y, int32_t y_dtype, const int32_t *topk_idx, const float *topk_w,
@@ -95,7 +108,7 @@ void launch_matmul_tile(int dtype, const MatmulArgs &args, const MatmulChoice &c
 void launch_matmul_deep(int dtype, const MatmulArgs &args, const MatmulChoice &choice, void *workspace,
                         hipStream_t stream);
 void launch_matmul_few(int dtype, const MatmulArgs &args, const MatmulChoice &choice, hipStream_t stream);
-void launch_matmul_i8_tile(const MatmulI8Args &args, const MatmulChoice &choice, hipStream_t stream);
+void launch_matmul_int_tile(const MatmulIntArgs &args, const MatmulChoice &choice, hipStream_t stream);
 moe_status launch_matmul(const moe_linear_t *linear, const MatmulArgs &args, const MatmulChoice &choice,
                          void *workspace, hipStream_t stream);
 
@@ -113,14 +126,15 @@ moe_status check_quantize(const void *x, int32_t dtype, int64_t x_stride, int32_
                           const int8_t *codes, int64_t codes_stride, const float *scales, QuantizeArgs *args);
 void launch_quantize(int dtype, const QuantizeArgs &args, hipStream_t stream);
 
-moe_status check_linear_i8(const moe_linear_int_t *linear);
+moe_status check_linear_int(const moe_linear_int_t *linear);
 // Checks a call and fills the kernels' arguments.  quantize->rows > 0: x is to be quantised
 // into the workspace first.  *parts is the workspace of the product itself.
-moe_status prepare_matmul_i8(const moe_linear_int_t *linear, const void *x, int32_t x_dtype, int64_t x_stride,
+moe_status prepare_matmul_int(const moe_linear_int_t *linear, const void *x, int32_t x_dtype, int64_t x_stride,
                              const float *x_scale, int32_t rows, int32_t top_k, int32_t rows_mode,
                              const moe_plan_t *plan, const void *residual, int32_t residual_dtype,
                              int64_t residual_stride, void *out, int64_t out_stride, void *workspace,
-                             size_t workspace_bytes, MatmulI8Args *args, MatmulChoice *choice,
+                             size_t workspace_bytes, MatmulIntFewArgs *args, MatmulChoice *choice,
                              QuantizeArgs *quantize, void **parts);
+void launch_matmul_int_few(int x_dtype, const MatmulIntFewArgs &args, const MatmulChoice &choice, hipStream_t stream);
 
 }  // namespace moe

@@ -1,87 +1,17 @@
 // Rows to 8-bit integers with a scale each (gfx950): moe_quantize_rows, and the first launch of the
-// integer products on activations that come in fp32, bf16 or fp16.
+// integer products on large batches in fp32, bf16 or fp16.
 //
-// code = x * 127 / m to the nearest integer, ties to even, m = max |x| of the row.  The codes are
-// those of the exact quotient, so that every way of computing them by this definition agrees:
-// t = x * (127 / m) with one rounding of the factor is off by at most 127 * 2^-24 = 7.6e-6,
-// which matters only where t lies that near to the middle between two integers; there
-// (0.5 - 2^-14 and more from its integer, one in 8000 elements) 64 bits decide, in which x * 127 is exact and the
-// quotient's rounding cannot cross the middle: a quotient of 31- by 24-bit integers that is
-// not the middle is at least 2^-32 of itself away from it.
-//
-// A wave (or four) holds a row in registers between the two passes, 16 bytes a load; longer rows
-// are read twice.
+// A wave (or four, for long rows and for few) holds a row in registers between the two passes, 16
+// bytes a load; longer rows are read twice.  A load covers the E values of its chunk, the last
+// one the last E of the row, which overlaps the one before: so all loads are whole and none
+// is behind a branch, where the compiler would wait for those before it.  HBM bounds it: 16384 rows of 2048 in
+// bf16, 101 MB, 23.6 us.
 #include <hip/hip_runtime.h>
 
-#include "matmul_device.h"
 #include "matmul_internal.h"
+#include "quantize_device.h"
 
 namespace moe {
-
-constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: adding it rounds to an integer, held in the low bits
-
-// A chunk's elements, widened.
-template <int DT>
-__device__ __forceinline__ void widen(const mm_u32x4 &v, float *f) {
-    if constexpr (DT == MOE_DTYPE_F32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint16_t b = (uint16_t)(i % 2 ? v[i / 2] >> 16 : v[i / 2]);
-            f[i] = DT == MOE_DTYPE_BF16 ? bf16_bits_to_f32(b) : f16_bits_to_f32(b);
-        }
-    }
-}
-
-// The largest |bits| of a chunk: ordered as the values are, infinity and then NaN above all.
-template <int DT>
-__device__ __forceinline__ uint32_t top_bits(const mm_u32x4 &v, uint32_t top) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (DT == MOE_DTYPE_F32) {
-            top = max(top, v[i] & 0x7FFFFFFFu);
-        } else {
-            top = max(top, v[i] & 0x7FFFu);
-            top = max(top, (v[i] >> 16) & 0x7FFFu);
-        }
-    }
-    return top;
-}
-
-struct RowScale {
-    float m, factor, pre;  // largest |x| and 127 / m, both of rows times pre
-};
-
-template <int DT>
-__device__ __forceinline__ void chunk_codes(const mm_u32x4 &v, const RowScale &s, uint32_t *out) {
-    constexpr int E = kChunk<DT>;
-    float f[E];
-    widen<DT>(v, f);
-    if (s.pre != 1.0f) {  // the same for the whole row
-#pragma unroll
-        for (int i = 0; i < E; ++i) f[i] *= s.pre;
-    }
-    uint32_t b[E];
-    float far = 0.f;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float r = fmaf(f[i], s.factor, kMagic);
-        b[i] = __float_as_uint(r);
-        far = fmaxf(far, fabsf(fmaf(f[i], s.factor, kMagic - r)));
-    }
-    if (far > 0.49993896484375f) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float q = (float)rint((double)f[i] * 127.0 / (double)s.m);
-            b[i] = __float_as_uint(q + kMagic);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < E; i += 4)
-        out[i / 4] = (b[i] & 0xFFu) | (b[i + 1] & 0xFFu) << 8 | (b[i + 2] & 0xFFu) << 16 | b[i + 3] << 24;
-}
 
 template <int E>
 struct __attribute__((packed, aligned(1))) Codes {
@@ -94,20 +24,24 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a) {
     constexpr int E = kChunk<DT>, T = 64 * W, ROWS = 4 / W;
     __shared__ uint32_t tops[4];
     const int tid = threadIdx.x % T;
-    const int chunks = (a.cols + E - 1) / E;
+    const int chunks = (a.cols + E - 1) / E, last = a.cols - E;  // a row has a chunk at least
     for (int64_t row0 = (int64_t)blockIdx.x * ROWS; row0 < a.rows; row0 += (int64_t)gridDim.x * ROWS) {
         const int64_t row = row0 + threadIdx.x / T;
         if (W == 1 && row >= a.rows) break;  // uniform in the wave, and no barriers then
         const char *x = a.x + row * a.x_stride;
+        int8_t *codes = a.codes + row * a.codes_stride;
+        auto first = [&](int c) { return c * E < last ? c * E : last; };
+        auto load = [&](int c) { return load_whole<DT, false>(x + (int64_t)first(c) * kElemBytes<DT>); };
         mm_u32x4 v[U ? U : 1];
         uint32_t top = 0;
         if constexpr (U > 0) {
 #pragma unroll
-            for (int i = 0; i < U; ++i) v[i] = load_chunk<DT, false>(x, tid + i * T, a.cols);
+            for (int i = 0; i < U; ++i) v[i] = load(tid + i * T);
 #pragma unroll
             for (int i = 0; i < U; ++i) top = top_bits<DT>(v[i], top);
         } else {
-            for (int c = tid; c < chunks; c += T) top = top_bits<DT>(load_chunk<DT, false>(x, c, a.cols), top);
+#pragma unroll 4
+            for (int c = tid; c < chunks; c += T) top = top_bits<DT>(load(c), top);
         }
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, off, kWave));
@@ -118,40 +52,37 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeArgs a) {
 #pragma unroll
             for (int i = 0; i < W; ++i) top = max(top, tops[i]);
         }
-        constexpr uint32_t kInf = DT == MOE_DTYPE_F32 ? 0x7F800000u : DT == MOE_DTYPE_BF16 ? 0x7F80u : 0x7C00u;
-        float m;
-        if constexpr (DT == MOE_DTYPE_F32)
-            m = __uint_as_float(top);
-        else
-            m = DT == MOE_DTYPE_BF16 ? bf16_bits_to_f32(top) : f16_bits_to_f32((uint16_t)top);
-        const bool finite = top < kInf;
-        if (tid == 0) a.scales[row] = finite ? m / 127.0f : __uint_as_float(0x7FC00000u);
-        // the factor 127 / m has to be a normal number: rows of very small or large values are brought near 1 first
-        RowScale s;
-        s.pre = m < 0x1p-100f ? 0x1p100f : m > 0x1p100f ? 0x1p-100f : 1.0f;
-        s.m = m * s.pre;
-        s.factor = finite && m > 0.f ? 127.0f / s.m : 0.f;
-        if (!finite || m == 0.f) s.m = 1.f;
+        const RowScale s = row_scale<DT>(top);
+        if (tid == 0) a.scales[row] = s.scale;
         auto put = [&](const mm_u32x4 &x4, int c) {
-            if (c * E >= a.codes_end) return;
-            uint32_t q[E / 4] = {};
-            if (finite && c < chunks) chunk_codes<DT>(x4, s, q);
-            int8_t *to = a.codes + row * a.codes_stride + (int64_t)c * E;
-            if ((c + 1) * E <= a.codes_end) {
-                Codes<E> w;
+            uint32_t q[E / 4];
+            chunk_codes<DT>(x4, s, q);
+            Codes<E> w;
 #pragma unroll
-                for (int i = 0; i < E / 4; ++i) w.v[i] = q[i];
-                *(Codes<E> *)to = w;
-            } else {
-                for (int i = 0; i < a.codes_end - c * E; ++i) to[i] = (int8_t)(q[i / 4] >> (8 * (i % 4)));
-            }
+            for (int i = 0; i < E / 4; ++i) w.v[i] = q[i];
+            if (c < chunks) *(Codes<E> *)(codes + first(c)) = w;
         };
         if constexpr (U > 0) {
 #pragma unroll
             for (int i = 0; i < U; ++i) put(v[i], tid + i * T);
         } else {
-            for (int c = tid; c * E < a.codes_end; c += T) put(load_chunk<DT, false>(x, c, a.cols), c);
+            for (int c = tid; c < chunks; c += T) put(load(c), c);
         }
+        if (tid < a.codes_end - a.cols) codes[a.cols + tid] = 0;  // at most 15
+    }
+}
+
+// Rows shorter than a chunk: a thread a row, element by element.
+template <int DT>
+__global__ __launch_bounds__(256) void quantize_short_kernel(QuantizeArgs a) {
+    for (int64_t row = (int64_t)blockIdx.x * 256 + threadIdx.x; row < a.rows; row += (int64_t)gridDim.x * 256) {
+        const mm_u32x4 v = load_chunk<DT, false>(a.x + row * a.x_stride, 0, a.cols);
+        const RowScale s = row_scale<DT>(top_bits<DT>(v, 0));
+        uint32_t q[kChunk<DT> / 4];
+        chunk_codes<DT>(v, s, q);
+        a.scales[row] = s.scale;
+        for (int i = 0; i < a.codes_end; ++i)
+            a.codes[row * a.codes_stride + i] = i < a.cols ? (int8_t)(q[i / 4] >> (8 * (i % 4))) : (int8_t)0;
     }
 }
 
@@ -163,11 +94,24 @@ static void launch_form(const QuantizeArgs &a, hipStream_t s) {
 
 template <int DT>
 static void launch_dtype(const QuantizeArgs &a, hipStream_t s) {
-    const int chunks = (a.codes_end + kChunk<DT> - 1) / kChunk<DT>;
-    if (chunks <= 64 * 2)
+    const int chunks = (a.cols + kChunk<DT> - 1) / kChunk<DT>;
+    if (a.cols < kChunk<DT>) {
+        const int64_t blocks = ((int64_t)a.rows + 255) / 256;
+        hipLaunchKernelGGL(quantize_short_kernel<DT>, dim3((unsigned)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, s, a);
+    } else if (chunks <= 64)
+        launch_form<DT, 1, 1>(a, s);
+    else if (chunks <= 64 * 2)
         launch_form<DT, 1, 2>(a, s);
+    else if (chunks <= 64 * 4 && a.rows >= 1024)
+        launch_form<DT, 1, 4>(a, s);
+    else if (chunks <= 64 * 8 && a.rows >= 1024)
+        launch_form<DT, 1, 8>(a, s);
+    else if (chunks <= 256)
+        launch_form<DT, 4, 1>(a, s);
     else if (chunks <= 256 * 2)
         launch_form<DT, 4, 2>(a, s);
+    else if (chunks <= 256 * 4)
+        launch_form<DT, 4, 4>(a, s);
     else if (chunks <= 256 * 8)
         launch_form<DT, 4, 8>(a, s);
     else

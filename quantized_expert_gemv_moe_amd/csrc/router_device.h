@@ -26,7 +26,7 @@ __device__ __forceinline__ uint64_t order_key(double v) {
 }
 
 // e^x = 2^n e^r, |r| <= ln 2 / 2, by the power series to r^13, whose rest is below r^14 / 14! = 5e-18 of it.
-// 0 below -745, infinity above 709.  (Short code: what runs once comes out of the instruction cache slowly.)
+// 0 below -745, infinity above 709.
 __device__ __forceinline__ double exp64(double x) {
     x = fmin(fmax(x, -1000.0), 1000.0);
     const double n = rint(x * 1.4426950408889634);
@@ -293,7 +293,8 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
 // keys of m and more wrap round to the far end: three instructions for two keys, and none
 // is taken out.  One more round than top_k shows that the last choice is clear as well.  Where choices
 // are not clear, sixteen of them are put in the order of their 64-bit values (some 4 tokens of 8192); the
-// whole wave's way, for what is then still open, takes 5 us longer, as its code is cold.
+// whole wave's way, for what is then still open, takes 5 us longer: a wave alone on its SIMD starts an
+// instruction every 3 ns.
 //
 // What bounds it: the instructions, some 200 a token of 256 experts.  8192 tokens of 256 experts, biased
 // and grouped: 20.2 us with a wave a token in 64 bits throughout, 7.3 so; 16384 of 128, plain:
