@@ -585,7 +585,8 @@ moe_status moe_router_topk(const moe_router_t *router, const void *logits, int32
                            int64_t logits_stride, int32_t n_tokens, int32_t *topk_idx, float *topk_w,
                            void *hip_stream);
 
-/* moe_router_topk, then moe_expert_plan of its choice: one launch for up to 16 tokens.
+/* moe_router_topk, then moe_expert_plan of its choice: one launch for up to 64 tokens of up
+ * to 512 experts in up to 16 groups.
  * n_tokens == 0 writes an empty plan. */
 moe_status moe_router_plan(const moe_router_t *router, const void *logits, int32_t logits_dtype,
                            int64_t logits_stride, int32_t n_tokens, int32_t *topk_idx, float *topk_w,

@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(BUILD_DIR, LIB_NAME)
 SOURCES = ["abi.cpp", "route.hip", "expert.hip", "gate_up_route.hip", "generic.hip", "pack.hip", "router_proj.hip", "tile.hip",
            "matmul_abi.cpp", "matmul.hip", "matmul_tile.hip", "matmul_deep.hip", "matmul_few.hip",
            "combine.hip", "router_abi.cpp", "router_topk.hip", "matmul_int_abi.cpp", "quantize.hip", "matmul_int.hip",
-           "matmul_int_tile.hip", "matmul_int_few.hip"]
+           "matmul_int_tile.hip", "matmul_int_tile4.hip", "matmul_int_few.hip"]
 ARCH = "gfx950"
 
 

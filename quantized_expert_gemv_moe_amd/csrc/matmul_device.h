@@ -133,6 +133,9 @@ struct __attribute__((packed, aligned(4))) Floats4 {
 struct __attribute__((packed, aligned(2))) Halves4 {
     mm_u32x2 v;
 };
+struct __attribute__((packed, aligned(2))) Halves8 {
+    mm_u32x4 v;
+};
 
 // Four consecutive values of a runtime dtype, widened.
 __device__ __forceinline__ mm_f32x4 load_value4(const void *p, int64_t i, int dtype) {

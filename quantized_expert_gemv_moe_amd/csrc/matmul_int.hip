@@ -16,7 +16,7 @@ static moe_status launch_int(const MatmulIntFewArgs &a, const MatmulChoice &c, c
     if (q.rows > 0) launch_quantize(x_dtype, q, s);
     switch (c.kernel) {
         case kMatmulIntFew: launch_matmul_int_few(x_dtype, a, c, s); break;
-        case kMatmulTile: launch_matmul_int_tile(a, c, s); break;
+        case kMatmulTile: c.mt == 8 ? launch_matmul_int_tile8(a, c, s) : launch_matmul_int_tile4(a, c, s); break;
         case kMatmulDeep: launch_deep_dtype<MOE_DTYPE_I8>(a, c, parts, s); break;
         case kMatmulFew: launch_few_dtype<MOE_DTYPE_I8>(a, c, s); break;
         default: launch_any_dtype<MOE_DTYPE_I8>(a, c, s); break;

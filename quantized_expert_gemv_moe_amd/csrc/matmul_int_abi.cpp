@@ -13,6 +13,7 @@ static int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 constexpr int64_t kMaxRowBytes = 1 << 24;
+constexpr int64_t kCopyRows = 256;
 constexpr int64_t kMaxGroupElems = (int64_t)1 << 40;
 
 moe_status check_quantize(const void *x, int32_t dtype, int64_t x_stride, int32_t n_rows, int32_t n_cols,
@@ -156,23 +157,37 @@ moe_status prepare_matmul_int(const moe_linear_int_t *L, const void *x, int32_t 
     int64_t px_stride = x_stride;
     const IntWorkspace w = int_workspace(x_rows, K);
     size_t used = 0;
-    if (own && rows > 0) {
+    // Integers whose rows do not fill whole chunks at 16-byte addresses are copied into such rows where the weights' do: a
+    // pass over x for the kernels of aligned rows (49216 rows, 1987 -> 704 into fp32: 316 us from where they are, COPYT so).
+    // Few rows stay, and so do those that the caller's workspace has no room for.
+    bool copied = false;
+    if (!own && rows > 0 && K >= 16 && linear_aligned(&view, L->row_tail) && x_rows >= kCopyRows &&
+        (K % 16 || !aligned(x, 16) || stride_or(x_stride, K) % 16) && workspace && aligned(workspace, 256))
+        copied = workspace_bytes >= w.parts + product_workspace(&view, rows, rows_mode != kRowsDense);
+    if ((own || copied) && rows > 0) {
         if (rows > INT32_MAX / 2) return MOE_ERR_UNSUPPORTED;
         if (!workspace || !aligned(workspace, 256)) return MOE_ERR_INVALID_ARG;
         used = w.parts;
         if (workspace_bytes < used) return MOE_ERR_WORKSPACE;
         px = workspace;
         px_stride = w.stride;
-        x_scale = (const float *)((char *)workspace + w.scales);
         *parts = (char *)workspace + used;
-        st = check_quantize(x, x_dtype, x_stride, (int32_t)x_rows, L->in_features, (int8_t *)workspace, w.stride, x_scale,
-                            quantize);
-        if (st != MOE_OK) return st;
+        if (own) {
+            x_scale = (const float *)((char *)workspace + w.scales);
+            st = check_quantize(x, x_dtype, x_stride, (int32_t)x_rows, L->in_features, (int8_t *)workspace, w.stride,
+                                x_scale, quantize);
+            if (st != MOE_OK) return st;
+        } else {
+            const int64_t xs = stride_or(x_stride, K);
+            if (xs < K) return MOE_ERR_INVALID_ARG;
+            if (xs >= kMaxRowBytes) return MOE_ERR_UNSUPPORTED;
+            *quantize = QuantizeArgs{(const char *)x, (int8_t *)workspace, nullptr, xs, w.stride, (int)x_rows, (int)K, 0};
+        }
         quantize->codes_end = (int)w.stride;
     }
     // rows of w may be read to the end of their last chunk where x's own rows are
     // padded as well
-    const int32_t tail = own || K % 16 == 0 ? L->row_tail : 0;
+    const int32_t tail = own || copied || K % 16 == 0 ? L->row_tail : 0;
     const int32_t fit = tail && (K + tail) % 16 == 0 ? tail : 0;
     st = prepare_product(&view, (int32_t)dtype_size(L->bias_dtype), fit, px, px_stride, rows, top_k, rows_mode, plan, residual,
                          residual_dtype, residual_stride, out, out_stride, *parts, workspace_bytes - used, a, choice);

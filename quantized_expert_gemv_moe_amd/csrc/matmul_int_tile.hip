@@ -1,10 +1,10 @@
-// Large tiles of the 8-bit integer products: their instantiations (the kernel is in matmul_tile.h).
+// The 256 x 256 tile of the 8-bit integer products: its instantiations (the kernel is in matmul_tile.h).
 #include "matmul_tile.h"
 
 namespace moe {
 
-void launch_matmul_int_tile(const MatmulIntArgs &a, const MatmulChoice &c, hipStream_t s) {
-    launch_tile_dtype<MOE_DTYPE_I8>(a, c, s);
+void launch_matmul_int_tile8(const MatmulIntArgs &a, const MatmulChoice &c, hipStream_t s) {
+    a.w_up ? launch_tile<MOE_DTYPE_I8, true, 8, 8>(a, c, s) : launch_tile<MOE_DTYPE_I8, false, 8, 8>(a, c, s);
 }
 
 }  // namespace moe

@@ -108,12 +108,14 @@ void launch_matmul_tile(int dtype, const MatmulArgs &args, const MatmulChoice &c
 void launch_matmul_deep(int dtype, const MatmulArgs &args, const MatmulChoice &choice, void *workspace,
                         hipStream_t stream);
 void launch_matmul_few(int dtype, const MatmulArgs &args, const MatmulChoice &choice, hipStream_t stream);
-void launch_matmul_int_tile(const MatmulIntArgs &args, const MatmulChoice &choice, hipStream_t stream);
+void launch_matmul_int_tile8(const MatmulIntArgs &args, const MatmulChoice &choice, hipStream_t stream);
+void launch_matmul_int_tile4(const MatmulIntArgs &args, const MatmulChoice &choice, hipStream_t stream);
 moe_status launch_matmul(const moe_linear_t *linear, const MatmulArgs &args, const MatmulChoice &choice,
                          void *workspace, hipStream_t stream);
 
 // --------------------------------------------------- 8-bit integer products
-// Rows to be quantised: x of a float type into codes and scales.  codes rows are
+// Rows to be quantised: x of a float type into codes and scales, or of 8-bit integers (16 and more to a
+// row) copied.  codes rows are
 // codes_stride bytes apart; the bytes from n_cols up to codes_end of a row are set to zero.
 struct QuantizeArgs {
     const char *x;

@@ -31,6 +31,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "matmul_device.h"
 #include "matmul_internal.h"
 #include "matmul_lds.h"
@@ -85,7 +87,7 @@ __device__ __forceinline__ void settle(mm_f32x4 (*c)[NT]) {
 }
 
 template <int DT, bool GATED, int MT, int NT>
-__global__ __launch_bounds__(256, 1) void matmul_tile_kernel(Args<DT> a) {
+__global__ __launch_bounds__(256, DT == MOE_DTYPE_I8 && MT * NT < 64 ? 2 : 1) void matmul_tile_kernel(Args<DT> a) {
     constexpr int BM = 32 * MT;                      // rows of x; of w 32 NT
     constexpr int NTC = GATED ? NT / 2 : NT;         // column tiles of a wave
     constexpr int CW = NTC * 16;                     // columns of a wave
@@ -275,21 +277,28 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(Args<DT> a) {
     const int col = col0 + wn * CW + lane_col<NTC>(g);
     auto row_of = [&](int m) { return wm * 16 * MT + m * 16 + r16; };
     if constexpr (DT != MOE_DTYPE_F32) {
-        if (a.vec_out == 2 && a.out_dtype != MOE_DTYPE_F32 && (DT == MOE_DTYPE_I8 || a.out_dtype == DT) &&
+        // (integer products: any output type at any address, as their own type says nothing of it)
+        constexpr bool INT = DT == MOE_DTYPE_I8;
+        if ((INT ? !a.residual || a.res_dtype == a.out_dtype : a.vec_out == 2 && a.out_dtype == DT) &&
             col0 + 2 * CW <= a.N) {
             mm_f32x4 b[NT], sc[NT];
             load_bias<DT, GATED, NT>(a, t.group, col, b);
             load_scales<DT, GATED, NT>(a, t.group, col, sc);
             auto straight = [&](auto f, auto has_residual, auto out_type) __attribute__((always_inline)) {
                 constexpr int OT = decltype(out_type)::value;
+                typedef typename std::conditional<OT == MOE_DTYPE_F32, float, uint16_t>::type Out;
+                constexpr int LW = OT == MOE_DTYPE_F32 ? 2 : 1;  // 16-byte words of eight columns
                 // a row's residual is fetched while the row before is finished
-                mm_u32x4 res[2][has_residual ? NTC / 2 : 1];
+                mm_u32x4 res[2][has_residual ? NTC / 2 : 1][LW];
                 auto fetch = [&](auto m) __attribute__((always_inline)) {
                     if constexpr (has_residual) {
                         const int o = orow[row_of(m)];
-                        const uint16_t *p = (const uint16_t *)a.residual + (int64_t)(o < 0 ? 0 : o) * a.res_stride + col;
+                        const Out *p = (const Out *)a.residual + (int64_t)(o < 0 ? 0 : o) * a.res_stride + col;
 #pragma unroll
-                        for (int n = 0; n < NTC; n += 2) res[m % 2][n / 2] = *(const mm_u32x4 *)(p + acc_col<NTC>(n));
+                        for (int n = 0; n < NTC; n += 2)
+#pragma unroll
+                            for (int k = 0; k < LW; ++k)
+                                res[m % 2][n / 2][k] = load_whole<OT, !INT>((const char *)(p + acc_col<NTC>(n) + 4 * k));
                     }
                 };
                 fetch(Index<0>{});
@@ -308,7 +317,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(Args<DT> a) {
                             for (int r = 0; r < 4; ++r) z[n][r] = clip(z[n][r], a.clamp);
                     }
                     const int o = orow[row_of(m)];
-                    uint16_t *p = (uint16_t *)a.out + (int64_t)(o < 0 ? 0 : o) * a.out_stride + col;
+                    Out *p = (Out *)a.out + (int64_t)(o < 0 ? 0 : o) * a.out_stride + col;
 #pragma unroll
                     for (int n = 0; n < NTC; n += 2) {
                         float v[8];
@@ -317,30 +326,59 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(Args<DT> a) {
                             v[i] = f(z[n + i / 4][i % 4]);
                             if constexpr (GATED) v[i] *= z[n + NTC + i / 4][i % 4];
                             if constexpr (has_residual) {
-                                const uint32_t w = res[m % 2][n / 2][i / 2];
-                                const uint16_t h = (uint16_t)(i % 2 ? w >> 16 : w);
-                                v[i] += OT == MOE_DTYPE_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+                                if constexpr (OT == MOE_DTYPE_F32) {
+                                    v[i] += __uint_as_float(res[m % 2][n / 2][i / 4][i % 4]);
+                                } else {
+                                    const uint32_t w = res[m % 2][n / 2][0][i / 2];
+                                    const uint16_t h = (uint16_t)(i % 2 ? w >> 16 : w);
+                                    v[i] += OT == MOE_DTYPE_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+                                }
                             }
                         }
-                        const mm_u32x4 w = {round_pair(v[0], v[1], OT), round_pair(v[2], v[3], OT),
-                                            round_pair(v[4], v[5], OT), round_pair(v[6], v[7], OT)};
-                        if (o >= 0) *(mm_u32x4 *)(p + acc_col<NTC>(n)) = w;
+                        if constexpr (OT == MOE_DTYPE_F32) {
+                            if (o >= 0) {
+                                ((Floats4 *)(p + acc_col<NTC>(n)))->v = mm_f32x4{v[0], v[1], v[2], v[3]};
+                                ((Floats4 *)(p + acc_col<NTC>(n) + 4))->v = mm_f32x4{v[4], v[5], v[6], v[7]};
+                            }
+                        } else {
+                            const mm_u32x4 w = {round_pair(v[0], v[1], OT), round_pair(v[2], v[3], OT),
+                                                round_pair(v[4], v[5], OT), round_pair(v[6], v[7], OT)};
+                            if constexpr (INT) {
+                                if (o >= 0) ((Halves8 *)(p + acc_col<NTC>(n)))->v = w;
+                            } else {
+                                if (o >= 0) *(mm_u32x4 *)(p + acc_col<NTC>(n)) = w;
+                            }
+                        }
                     }
                 });
             };
             auto either = [&](auto f) __attribute__((always_inline)) {
-                if (DT == MOE_DTYPE_I8 && a.out_dtype == MOE_DTYPE_F16) {
-                    if constexpr (DT == MOE_DTYPE_I8)
-                        a.residual ? straight(f, Yes{}, Index<MOE_DTYPE_F16>{}) : straight(f, No{}, Index<MOE_DTYPE_F16>{});
-                    return;
+                auto with = [&](auto out_type) __attribute__((always_inline)) {
+                    a.residual ? straight(f, Yes{}, out_type) : straight(f, No{}, out_type);
+                };
+                if constexpr (INT) {
+                    switch (a.out_dtype) {
+                        case MOE_DTYPE_BF16: with(Index<MOE_DTYPE_BF16>{}); break;
+                        case MOE_DTYPE_F16: with(Index<MOE_DTYPE_F16>{}); break;
+                        default: with(Index<MOE_DTYPE_F32>{}); break;
+                    }
+                } else {
+                    with(Index<DT>{});
                 }
-                constexpr int OT = DT == MOE_DTYPE_I8 ? (int)MOE_DTYPE_BF16 : DT;
-                a.residual ? straight(f, Yes{}, Index<OT>{}) : straight(f, No{}, Index<OT>{});
             };
             switch (a.fn) {
-                case MOE_FN_NONE: either([](float z) { return z; }); return;
+                case MOE_FN_NONE:
+                    if constexpr (INT && GATED) break;  // as good as never gated
+                    either([](float z) { return z; });
+                    return;
                 case MOE_FN_SILU: either([](float z) { return silu(z); }); return;
                 case MOE_FN_GELU_TANH: either([](float z) { return gelu_tanh(z); }); return;
+                case MOE_FN_RELU:
+                    if constexpr (INT && !GATED) {
+                        either([](float z) { return z < 0.f ? 0.f : z; });
+                        return;
+                    }
+                    break;
                 default: break;
             }
         }

@@ -55,7 +55,9 @@ moe_status prepare_router(const moe_router_t *r, const void *logits, int32_t dty
     a->per_group = r->n_experts / groups;
     a->top_groups = r->top_groups < groups ? r->top_groups : groups;
     a->top2 = r->group_score == MOE_GROUP_TOP2;
-    router_lanes(a, 64);
+    const int per_lane = router_per_lane(r->n_experts, groups);
+    a->seg = (a->per_group + per_lane - 1) / per_lane;
+    a->lane_magic = 65536 / a->seg + 1;
     return MOE_OK;
 }
 

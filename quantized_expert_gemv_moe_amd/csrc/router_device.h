@@ -279,8 +279,7 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
 }
 
 // ------------------------------------------------- four tokens a wave
-// Sixteen lanes a token, PL experts a lane, for up to 512 experts whose groups fill whole lanes:
-// most tokens are routed by 32-bit numbers with a proof that 64 bits would not choose otherwise,
+// Sixteen lanes a token, PL experts a lane, for up to 512 experts: most tokens are routed by 32-bit numbers with a proof that 64 bits would not choose otherwise,
 // the others (and those with masked experts or scores that are not numbers) by the whole wave
 // as above.
 //
@@ -335,19 +334,26 @@ __device__ __forceinline__ double row_sum(double v) {
 
 // Routes tokens t0 .. t0 + 3 (those below n_tokens) by the calling wave.  Lane 16 i + j returns token
 // t0 + i's j-th expert and its weight, for j < top_k; the result is valid where the token exists.
-// a.per_group is a multiple of PL, a group's lanes a power of two.
-template <int PL, int SLOW, bool BIAS, bool GROUPS>
+// A group's lanes (a.seg) are a power of two; WHOLE: every lane with experts has PL of them.
+template <int PL, int SLOW, bool WHOLE, bool BIAS, bool GROUPS>
 __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArgs &one, int64_t t0, int *id, float *weight) {
     const int lane = threadIdx.x & (kWave - 1), r = lane & 15, row0 = lane & 48;
     const int64_t t = t0 + (lane >> 4) < a.n_tokens ? t0 + (lane >> 4) : a.n_tokens - 1;
-    const bool live = r * PL < a.n_experts;
-    const int e0 = live ? r * PL : 0;  // lanes without experts repeat the first ones and leave them out of the choice
+    const int group = GROUPS ? (r * a.lane_magic) >> 16 : 0;
+    const int in_group = (GROUPS ? r - group * a.seg : r) * PL;
+    const int n = group >= a.n_groups ? 0 : WHOLE ? (in_group < a.per_group ? PL : 0) : a.per_group - in_group;
+    const bool live = n > 0;
+    // lanes without experts repeat the first ones, lanes with fewer than PL their last one; they are left out of
+    // the choice
+    const int e0 = live ? group * a.per_group + in_group : 0;
+    auto has = [&](int q) { return WHOLE || q < n; };
     constexpr float kNone = -INFINITY;
 
     float l[PL], c[PL];  // logits, and what the order goes by
     const int64_t at = t * a.stride;
-    load_lane<PL>(a.logits, at + e0, PL, true, a.dtype, l);
-    if constexpr (BIAS) load_lane_of<PL, MOE_DTYPE_F32>(a.bias, e0, PL, true, c);
+    const int there_are = WHOLE || n > PL ? PL : n;
+    load_lane<PL>(a.logits, at + e0, there_are, WHOLE, a.dtype, l);
+    if constexpr (BIAS) load_lane_of<PL, MOE_DTYPE_F32>(a.bias, e0, there_are, WHOLE, c);
     float l_min = l[0];
 #pragma unroll
     for (int q = 1; q < PL; ++q) l_min = fminf(l_min, l[q]);
@@ -366,8 +372,8 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
         for (int q = 0; q < PL; ++q) {
             const float e = expf(l[q] - top);
             if constexpr (BIAS || GROUPS) s[q] = e;
-            total += e;
-            if (!a.renormalise) sum += (double)e;
+            total += has(q) ? e : 0.f;
+            if (!a.renormalise) sum += has(q) ? (double)e : 0.0;
         }
         if (!a.renormalise) sum = row_sum(live ? sum : 0.0);
         largest = __builtin_amdgcn_rcpf(row_reduce(live ? total : 0.f, Add{}));
@@ -409,11 +415,14 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
         };
 #pragma unroll
         for (int q = 0; q < PL; ++q) {
+            float v;
             if constexpr (BIAS)
-                add(c[q]);
+                v = c[q];
             else
-                add(a.top2 ? s[q] : l[q]);
+                v = a.top2 ? s[q] : l[q];
+            add(has(q) ? v : kNone);
         }
+        if (!live) best = second = kNone;
         auto meet = [&](auto ctrl) {
             constexpr int C = decltype(ctrl)::value;
             const float ob = row_move<C>(best), os = row_move<C>(second);
@@ -423,7 +432,7 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
         if (a.seg >= 2) meet(Index<kXor1>{});
         if (a.seg >= 4) meet(Index<kXor2>{});
         if (a.seg >= 8) meet(Index<kHalfMirror>{});
-        const float mine = !live ? kNone : a.top2 && a.per_group > 1 ? best + second : best;
+        const float mine = a.top2 && a.per_group > 1 ? best + second : best;
         const float over = !scores ? mine : mine + 4.f * delta, under = !scores ? mine : mine - 4.f * delta;
         // lanes whose group is surely, or maybe, before this one's; without margins lanes of equal
         // groups to the left as well
@@ -435,7 +444,6 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
             maybe += other > under;
         });
         if (!scores) {
-            const int group = (r * a.lane_magic) >> 16;
             static_for<15>([&](auto i) {
                 constexpr int N = decltype(i)::value + 1;
                 const bool tie = row_move<0x120 + N>(mine) == mine && ((((r - N) & 15) * a.lane_magic) >> 16) < group;
@@ -457,7 +465,7 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
     uint32_t key[PL];
 #pragma unroll
     for (int q = 0; q < PL; ++q)
-        key[q] = ((uint32_t)fmaf(c[q] - lo, by, from) << 10) + (uint32_t)(1023 - r * PL) - q;
+        key[q] = has(q) ? ((uint32_t)fmaf(c[q] - lo, by, from) << 10) + (uint32_t)(1023 - e0) - q : 0u;
     const int all = a.top_groups * a.per_group;
     const bool chosen = r < a.top_k;
     uint32_t m = 0, my_key = 0;  // lane j has the j-th choice, the last one is m

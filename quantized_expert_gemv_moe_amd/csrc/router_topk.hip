@@ -22,14 +22,14 @@ __global__ __launch_bounds__(kBlock) void router_topk_kernel(RouterArgs a) {
 }
 
 // A wave four tokens; `one` has the lanes of a whole wave for a token, SLOW its experts a lane.
-template <int PL, int SLOW, bool BIAS, bool GROUPS>
+template <int PL, int SLOW, bool WHOLE, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(kBlock) void router_four_kernel(RouterArgs a, RouterArgs one) {
     const int64_t t0 = ((int64_t)blockIdx.x * (kBlock / kWave) + threadIdx.x / kWave) * 4;
     if (t0 >= a.n_tokens) return;  // uniform per wave
     const int lane = threadIdx.x & (kWave - 1);
     int id;
     float w;
-    router_four<PL, SLOW, BIAS, GROUPS>(a, one, t0, &id, &w);
+    router_four<PL, SLOW, WHOLE, BIAS, GROUPS>(a, one, t0, &id, &w);
     const int64_t t = t0 + (lane >> 4);
     if (t < a.n_tokens && (lane & 15) < a.top_k) {
         a.idx[t * a.top_k + (lane & 15)] = id;
@@ -37,19 +37,19 @@ __global__ __launch_bounds__(kBlock) void router_four_kernel(RouterArgs a, Route
     }
 }
 
-// Router and planner in one workgroup, as route_plan_kernel: up to 16 tokens, the ids in
-// LDS as well, then one wave (up to 64 slots) or the whole block plans them.
-constexpr int kRouterPlanThreads = 1024;
+// Router and planner in one workgroup, as route_plan_kernel: up to 64 tokens, the ids in LDS as well, then one wave
+// (up to 64 slots) or the whole block plans them.
+constexpr int kRouterPlanThreads = 1024, kRouterPlanTokens = 64;
 
-template <int PL, int SLOW, bool BIAS, bool GROUPS>
+template <int PL, int SLOW, bool WHOLE, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(kRouterPlanThreads) void router_plan_kernel(RouterArgs a, RouterArgs one, PlanOut p) {
-    __shared__ int idx_lds[kRoutePlanMaxSlots];
+    __shared__ int idx_lds[kRouterPlanTokens * MOE_MAX_TOP_K];
     const int lane = threadIdx.x & (kWave - 1);
     const int64_t t0 = threadIdx.x / kWave * 4;
     if (t0 < a.n_tokens) {
         int id;
         float w;
-        router_four<PL, SLOW, BIAS, GROUPS>(a, one, t0, &id, &w);
+        router_four<PL, SLOW, WHOLE, BIAS, GROUPS>(a, one, t0, &id, &w);
         const int64_t t = t0 + (lane >> 4);
         if (t < a.n_tokens && (lane & 15) < a.top_k) {
             const int s = (int)t * a.top_k + (lane & 15);
@@ -77,8 +77,8 @@ static void pick_flags(const RouterArgs &a, F &&f) {
         a.bias ? f(Index<PL>{}, Index<1>{}, Index<0>{}) : f(Index<PL>{}, Index<0>{}, Index<0>{});
 }
 template <class F>
-static moe_status pick(const RouterArgs &a, int lanes, F &&f) {
-    switch (router_per_lane(a.n_experts, a.n_groups, lanes)) {
+static moe_status pick(const RouterArgs &a, int per_lane, F &&f) {
+    switch (per_lane) {
         case 1: pick_flags<1>(a, f); break;
         case 2: pick_flags<2>(a, f); break;
         case 4: pick_flags<4>(a, f); break;
@@ -89,31 +89,41 @@ static moe_status pick(const RouterArgs &a, int lanes, F &&f) {
     return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
 
-// Experts a lane of a whole wave where 16 lanes hold PL each, and the arguments of such a wave.
+// Experts a lane of a whole wave where 16 lanes hold PL each, and the arguments of such a wave and of those lanes.
 template <int PL>
 constexpr int kSlow = PL <= 4 ? 1 : PL / 4;
-template <int PL>
-static RouterArgs for_one(RouterArgs a) {
-    a.seg = (a.per_group + kSlow<PL> - 1) / kSlow<PL>;
-    a.lane_magic = 65536 / a.seg + 1;
+static RouterArgs with_lanes(RouterArgs a, int seg) {
+    a.seg = seg;
+    a.lane_magic = 65536 / seg + 1;
     return a;
+}
+template <int PL>
+static RouterArgs for_one(const RouterArgs &a) {
+    return with_lanes(a, (a.per_group + kSlow<PL> - 1) / kSlow<PL>);
 }
 
 static moe_status launch_topk(const RouterArgs &one, hipStream_t stream) {
-    if (!router_by_fours(one.n_experts, one.n_groups)) {
+    int seg;
+    const int per_lane = router_four_lanes(one.n_experts, one.n_groups, &seg);
+    if (!per_lane) {
         const unsigned blocks = (unsigned)((one.n_tokens + (int64_t)kBlock / kWave - 1) / (kBlock / kWave));
-        return pick(one, 64, [&](auto pl, auto bias, auto groups) {
-            if constexpr (groups.value || pl.value <= 16)  // 1024 experts without groups
+        return pick(one, router_per_lane(one.n_experts, one.n_groups), [&](auto pl, auto bias, auto groups) {
+            if constexpr (groups.value || pl.value == 16)  // without groups only more than 512 experts come here
                 hipLaunchKernelGGL((router_topk_kernel<pl.value, bias.value != 0, groups.value != 0>), dim3(blocks),
                                    dim3(kBlock), 0, stream, one);
         });
     }
-    RouterArgs a = one;
-    router_lanes(&a, 16);
+    const RouterArgs a = with_lanes(one, seg);
     const unsigned blocks = (unsigned)((a.n_tokens + (int64_t)kBlock / 16 - 1) / (kBlock / 16));
-    return pick(a, 16, [&](auto pl, auto bias, auto groups) {
-        hipLaunchKernelGGL((router_four_kernel<pl.value, kSlow<pl.value>, bias.value != 0, groups.value != 0>), dim3(blocks),
-                           dim3(kBlock), 0, stream, a, for_one<pl.value>(a));
+    return pick(a, per_lane, [&](auto pl, auto bias, auto groups) {
+        constexpr int PL = pl.value;
+        constexpr bool B = bias.value != 0, G = groups.value != 0;
+        if (a.per_group % PL == 0)
+            hipLaunchKernelGGL((router_four_kernel<PL, kSlow<PL>, true, B, G>), dim3(blocks), dim3(kBlock), 0, stream, a,
+                               for_one<PL>(a));
+        else
+            hipLaunchKernelGGL((router_four_kernel<PL, kSlow<PL>, false, B, G>), dim3(blocks), dim3(kBlock), 0, stream, a,
+                               for_one<PL>(a));
     });
 }
 
@@ -139,7 +149,9 @@ extern "C" moe_status moe_router_plan(const moe_router_t *router, const void *lo
     st = check_plan_args(topk_idx, n_tokens, router->n_experts, router->top_k, plan);
     if (st != MOE_OK) return st;
     hipStream_t stream = (hipStream_t)hip_stream;
-    if (n_tokens == 0 || n_tokens > kRoutePlanMaxTokens || !router_by_fours(one.n_experts, one.n_groups)) {
+    int seg;
+    const int per_lane = router_four_lanes(one.n_experts, one.n_groups, &seg);
+    if (n_tokens == 0 || n_tokens > kRouterPlanTokens || !per_lane) {
         if (n_tokens > 0) st = launch_topk(one, stream);
         if (st != MOE_OK) return st;
         return moe_expert_plan(topk_idx, n_tokens, router->n_experts, router->top_k, plan, hip_stream);
@@ -147,10 +159,15 @@ extern "C" moe_status moe_router_plan(const moe_router_t *router, const void *lo
     const int threads = n_tokens * router->top_k <= kWave ? kWave * ((n_tokens + 3) / 4) : kRouterPlanThreads;
     const PlanOut out{plan->counts, plan->offsets, plan->sorted_slots, plan->unique_experts, plan->n_unique,
                       (int4 *)plan->work};
-    RouterArgs a = one;
-    router_lanes(&a, 16);
-    return pick(a, 16, [&](auto pl, auto bias, auto groups) {
-        hipLaunchKernelGGL((router_plan_kernel<pl.value, kSlow<pl.value>, bias.value != 0, groups.value != 0>), dim3(1),
-                           dim3(threads), 0, stream, a, for_one<pl.value>(a), out);
+    const RouterArgs a = with_lanes(one, seg);
+    return pick(a, per_lane, [&](auto pl, auto bias, auto groups) {
+        constexpr int PL = pl.value;
+        constexpr bool B = bias.value != 0, G = groups.value != 0;
+        if (a.per_group % PL == 0)
+            hipLaunchKernelGGL((router_plan_kernel<PL, kSlow<PL>, true, B, G>), dim3(1), dim3(threads), 0, stream, a,
+                               for_one<PL>(a), out);
+        else
+            hipLaunchKernelGGL((router_plan_kernel<PL, kSlow<PL>, false, B, G>), dim3(1), dim3(threads), 0, stream, a,
+                               for_one<PL>(a), out);
     });
 }

@@ -109,7 +109,7 @@ def test_router_refusals():
 
 
 def test_every_shape_has_lanes_for_its_groups():
-    """The kernels' division of a wave, as router_per_lane makes it."""
+    """The kernels' division of a wave, as router_per_lane and router_four_lanes make it."""
     def lanes(E, G):
         per, p = E // G, 1
         while p < 32 and -(-per // p) * G > 64:
