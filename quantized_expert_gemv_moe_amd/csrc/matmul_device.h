@@ -334,37 +334,54 @@ __device__ __forceinline__ void finish_row(const MatmulArgs &a, int o, int col, 
 }
 
 // The biases of a lane's columns (zero without one; -0, which changes no sum).
-// Columns from N on take the last column's; the store drops them.
-template <int DT, bool GATED, int NT>
+// Columns from N on take the last column's; the store drops them.  WHOLE: there are none of those.
+template <int DT, bool GATED, int NT, bool WHOLE = false>
 __device__ __forceinline__ void load_bias(const Args<DT> &a, int group, int col, mm_f32x4 *b) {
     constexpr int NC = GATED ? NT / 2 : NT;
 #pragma unroll
     for (int n = 0; n < NT; ++n) b[n] = mm_f32x4{-0.f, -0.f, -0.f, -0.f};
     if (!a.bias) return;
+    auto load = [&](auto dtype) __attribute__((always_inline)) {
+        constexpr int BT = decltype(dtype)::value;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const char *p = (n < NC ? a.bias : a.bias_up) + (int64_t)group * a.bias_group;
+        for (int n = 0; n < NT; ++n) {
+            const char *p = (n < NC ? a.bias : a.bias_up) + (int64_t)group * a.bias_group;
+            if constexpr (WHOLE) {
+                b[n] = load_value4(p, col + acc_col<NC>(n % NC), BT);
+                continue;
+            }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int c = col + acc_col<NC>(n % NC) + r;
-            if constexpr (DT == MOE_DTYPE_I8)
-                b[n][r] = load_value(p, c < a.N ? c : a.N - 1, a.bias_dtype);
-            else
-                b[n][r] = load_value(p, c < a.N ? c : a.N - 1, DT);
+            for (int r = 0; r < 4; ++r) {
+                const int c = col + acc_col<NC>(n % NC) + r;
+                b[n][r] = load_value(p, c < a.N ? c : a.N - 1, BT);
+            }
         }
+    };
+    if constexpr (DT == MOE_DTYPE_I8) {  // any type, told apart once and not for every element
+        switch (a.bias_dtype) {
+            case MOE_DTYPE_BF16: load(Index<MOE_DTYPE_BF16>{}); break;
+            case MOE_DTYPE_F16: load(Index<MOE_DTYPE_F16>{}); break;
+            default: load(Index<MOE_DTYPE_F32>{}); break;
+        }
+    } else {
+        load(Index<DT>{});
     }
 }
 
 // What a lane's integer products are scaled with: a factor for each of its columns, as load_bias
 // has them, and one for the row.  A row's sum is rounded to fp32 once, the two factors'
 // product once and theirs once.  Nothing of it exists for the other types.
-template <int DT, bool GATED, int NT>
+template <int DT, bool GATED, int NT, bool WHOLE = false>
 __device__ __forceinline__ void load_scales(const Args<DT> &a, int group, int col, mm_f32x4 *sc) {
     if constexpr (DT == MOE_DTYPE_I8) {
         constexpr int NC = GATED ? NT / 2 : NT;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float *p = (n < NC ? a.w_scale : a.w_up_scale) + (int64_t)group * a.scale_group;
+            if constexpr (WHOLE) {
+                sc[n] = ((const Floats4 *)(p + col + acc_col<NC>(n % NC)))->v;
+                continue;
+            }
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const int c = col + acc_col<NC>(n % NC) + r;

@@ -158,7 +158,7 @@ moe_status prepare_matmul_int(const moe_linear_int_t *L, const void *x, int32_t 
     const IntWorkspace w = int_workspace(x_rows, K);
     size_t used = 0;
     // Integers whose rows do not fill whole chunks at 16-byte addresses are copied into such rows where the weights' do: a
-    // pass over x for the kernels of aligned rows (49216 rows, 1987 -> 704 into fp32: 316 us from where they are, COPYT so).
+    // pass over x for the kernels of aligned rows (49216 rows, 1987 -> 704 into fp32: 316 us from where they are, 178 so).
     // Few rows stay, and so do those that the caller's workspace has no room for.
     bool copied = false;
     if (!own && rows > 0 && K >= 16 && linear_aligned(&view, L->row_tail) && x_rows >= kCopyRows &&

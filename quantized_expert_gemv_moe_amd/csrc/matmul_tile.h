@@ -282,8 +282,13 @@ __global__ __launch_bounds__(256, DT == MOE_DTYPE_I8 && MT * NT < 64 ? 2 : 1) vo
         if ((INT ? !a.residual || a.res_dtype == a.out_dtype : a.vec_out == 2 && a.out_dtype == DT) &&
             col0 + 2 * CW <= a.N) {
             mm_f32x4 b[NT], sc[NT];
-            load_bias<DT, GATED, NT>(a, t.group, col, b);
-            load_scales<DT, GATED, NT>(a, t.group, col, sc);
+            load_bias<DT, GATED, NT, INT>(a, t.group, col, b);
+            load_scales<DT, GATED, NT, true>(a, t.group, col, sc);
+            // (all of a tile's factors at once: one row's after another, 8192 x 1024 x 2048 took
+            // 25.7 us, now 22.3, and 8192 x 8192 x 4096 194 and 189)
+            float xf[MT];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) xf[m] = x_factor<DT>(a, orow[row_of(m)]);
             auto straight = [&](auto f, auto has_residual, auto out_type) __attribute__((always_inline)) {
                 constexpr int OT = decltype(out_type)::value;
                 typedef typename std::conditional<OT == MOE_DTYPE_F32, float, uint16_t>::type Out;
@@ -307,7 +312,7 @@ __global__ __launch_bounds__(256, DT == MOE_DTYPE_I8 && MT * NT < 64 ? 2 : 1) vo
                     if constexpr (m + 1 < MT) fetch(Index<m + 1>{});
                     mm_f32x4 *z = acc[m];
                     if constexpr (ACC) hold<NT, m == MT - 1>(z);
-                    scale_row<DT, NT>(z, sc, x_factor<DT>(a, orow[row_of(m)]));
+                    scale_row<DT, NT>(z, sc, xf[m]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) z[n] += b[n];
                     if (a.clamp > 0.f) {
