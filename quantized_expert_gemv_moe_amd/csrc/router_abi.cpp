@@ -26,6 +26,7 @@ moe_status prepare_router(const moe_router_t *r, const void *logits, int32_t dty
     if (n_tokens < 0 || stride < 0 || (stride && stride < r->n_experts)) return MOE_ERR_INVALID_ARG;
     if ((int64_t)n_tokens * r->top_k > INT32_MAX / 2 || stride > (int64_t)1 << 32) return MOE_ERR_UNSUPPORTED;
     const int64_t es = (int64_t)dtype_size(dtype), row = stride ? stride : r->n_experts;
+    if (n_tokens > ((int64_t)1 << 60) / (row * es)) return MOE_ERR_UNSUPPORTED;
     if (n_tokens > 0) {
         if (!logits || !idx || !w || (uintptr_t)logits % es || (uintptr_t)idx % 4 || (uintptr_t)w % 4)
             return MOE_ERR_INVALID_ARG;
