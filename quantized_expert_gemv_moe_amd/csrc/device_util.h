@@ -71,4 +71,21 @@ __device__ __forceinline__ float dot32_q4(uint4 q, const float *x) {
     return (a0 + a1) + (a2 + a3);
 }
 
+// Inclusive prefix sum over the 64 lanes of a wave (DPP: row shifts, then
+// row broadcasts of lanes 15 and 31).  Lanes whose source is out of range
+// add 0.
+template <int CTRL, int ROW_MASK>
+__device__ __forceinline__ int dpp_add_src(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROW_MASK, 0xF, false);
+}
+__device__ __forceinline__ int wave_inclusive_scan(int v) {
+    v += dpp_add_src<0x111, 0xF>(v);  // row_shr:1
+    v += dpp_add_src<0x112, 0xF>(v);  // row_shr:2
+    v += dpp_add_src<0x114, 0xF>(v);  // row_shr:4
+    v += dpp_add_src<0x118, 0xF>(v);  // row_shr:8
+    v += dpp_add_src<0x142, 0xA>(v);  // row_bcast:15 into rows 1 and 3
+    v += dpp_add_src<0x143, 0xC>(v);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
 }  // namespace moe

@@ -411,23 +411,24 @@ struct MatmulTile {
 // Workgroup ids are dealt to the XCDs round robin.  Each XCD takes one
 // contiguous stretch of the order of tiles, so that tiles that share rows of x or of w
 // meet in one L2.
-__device__ __forceinline__ int64_t xcd_order(int64_t id, int64_t total) {
+// (A launch has at most 2^23 tiles, so 32 bits hold all of it: a 64-bit division is a hundred instructions.)
+__device__ __forceinline__ int xcd_order(int id, int total) {
     constexpr int kXcd = 8;
-    const int64_t chunk = (total + kXcd - 1) / kXcd;
-    const int64_t x = id % kXcd, j = id / kXcd;
-    const int64_t t = x * chunk + j;
+    const int chunk = (int)((unsigned)(total + kXcd - 1) / kXcd);
+    const int x = (int)((unsigned)id % kXcd), j = (int)((unsigned)id / kXcd);
+    const int t = x * chunk + j;
     return j < chunk && t < total ? t : -1;
 }
 
 // Dense: blocks of GM row tiles, all columns of a block before the next.
 template <int GM>
 __device__ __forceinline__ bool dense_tile(const MatmulArgs &a, int BM, int block, MatmulTile *t) {
-    const int64_t id = xcd_order(block, (int64_t)a.tiles_m * a.tiles_n);
+    const int id = xcd_order(block, a.tiles_m * a.tiles_n);
     if (id < 0) return false;
     const int per = GM * a.tiles_n;
-    const int g = (int)(id / per), r = (int)(id - (int64_t)g * per);
+    const int g = (int)((unsigned)id / (unsigned)per), r = id - g * per;
     const int gm = a.tiles_m - g * GM < GM ? a.tiles_m - g * GM : GM;
-    *t = MatmulTile{0, 0, a.rows, (g * GM + r % gm) * BM, r / gm, (int)id};
+    *t = MatmulTile{0, 0, a.rows, (g * GM + r % gm) * BM, r / gm, id};
     return true;
 }
 
@@ -437,11 +438,82 @@ __device__ __forceinline__ bool group_record(const MatmulArgs &a, int u, int4 *r
     return (unsigned)r->x < (unsigned)a.groups && r->y >= 0 && r->z >= 1 && r->y <= a.rows - r->z;
 }
 
+// Up to kHeldRecords records, four consecutive ones a lane, their row tiles and the tiles before them.
+struct HeldRecords {
+    static constexpr int PER = kHeldRecords / kWave;
+    int4 r[PER];
+    int tiles[PER];
+    int mine, incl;  // row tiles of the lane's records; of them and all before
+    __device__ __forceinline__ void load(const MatmulArgs &a, int BM) {
+        const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const int u = lane * PER + q;
+            r[q] = a.work[u < a.n_records ? u : 0];
+        }
+        mine = 0;
+#pragma unroll
+        for (int q = 0; q < PER; ++q) {
+            const bool good = lane * PER + q < a.n_records && (unsigned)r[q].x < (unsigned)a.groups && r[q].y >= 0 &&
+                              r[q].z >= 1 && r[q].y <= a.rows - r[q].z;
+            tiles[q] = good ? (r[q].z + BM - 1) / BM : 0;
+            mine += tiles[q];
+        }
+        // no plan of this call's slots has more than tiles_m row tiles; one that claims more
+        // (its records overlap) is cut there, so that tiles stay within the grid and the workspace
+        if (mine > a.tiles_m) mine = a.tiles_m;
+        incl = wave_inclusive_scan(mine);
+    }
+    // The record of row tile m, and the row tiles before it; false if there is none.
+    __device__ __forceinline__ bool find(int m, int4 *record, int *before) const {
+        int at = incl - mine;
+        const unsigned long long hit = __ballot(m >= at && m < incl);
+        if (!hit) return false;
+        const int src = __builtin_ctzll(hit);
+        int4 f = r[0];
+        int first = at;
+#pragma unroll
+        for (int q = 1; q < PER; ++q) {
+            at += tiles[q - 1];
+            const bool here = m >= at;
+            f.x = here ? r[q].x : f.x;
+            f.y = here ? r[q].y : f.y;
+            f.z = here ? r[q].z : f.z;
+            first = here ? at : first;
+        }
+        *record = make_int4(__builtin_amdgcn_readlane(f.x, src), __builtin_amdgcn_readlane(f.y, src),
+                            __builtin_amdgcn_readlane(f.z, src), 0);
+        *before = __builtin_amdgcn_readlane(first, src);
+        return true;
+    }
+};
+
 // Grouped: experts in the plan's order, within an expert all row tiles of a
 // column block before the next.  Every wave finds the tile by itself: each
 // lane sums the row tiles of a run of records, a wave scan places the runs,
-// and the lane whose run holds the tile finds its record.
+// and the lane whose run holds the tile finds its record: among those that it holds, or, of more than kHeldRecords,
+// by loading them again, which is two more trips to memory ahead of the first operand (32 tokens, top 8 of 128,
+// 768 -> 2048 in integers: 41.8 us so, held 37.4; 8192 tokens, 2048 -> 768 gated in bf16 416 and 410).
 __device__ __forceinline__ bool grouped_tile(const MatmulArgs &a, int BM, int block, MatmulTile *t) {
+    auto place = [&](int id, const int4 &r, int before) {
+        const int count = __builtin_amdgcn_readfirstlane(r.z);
+        const int nb = (count + BM - 1) / BM;
+        const int local = id - before * a.tiles_n;
+        *t = MatmulTile{__builtin_amdgcn_readfirstlane(r.x), __builtin_amdgcn_readfirstlane(r.y), count,
+                        (local % nb) * BM, local / nb, id};
+    };
+    if (a.n_records <= kHeldRecords) {
+        HeldRecords h;
+        h.load(a, BM);
+        const int all = __builtin_amdgcn_readlane(h.incl, kWave - 1);
+        const int id = xcd_order(block, (all < a.tiles_m ? all : a.tiles_m) * a.tiles_n);
+        if (id < 0) return false;
+        int4 r;
+        int before;
+        if (!h.find((int)((unsigned)id / (unsigned)a.tiles_n), &r, &before)) return false;
+        place(id, r, before);
+        return true;
+    }
     const int lane = threadIdx.x & (kWave - 1);
     const int per = (a.n_records + kWave - 1) / kWave;
     const int u0 = lane * per;
@@ -453,17 +525,11 @@ __device__ __forceinline__ bool grouped_tile(const MatmulArgs &a, int BM, int bl
     // no plan of this call's slots has more than tiles_m row tiles; one that claims more
     // (its records overlap) is cut there, so that tiles stay within the grid and the workspace
     if (mine > a.tiles_m) mine = a.tiles_m;
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const int v = __shfl_up(incl, d, kWave);
-        if (lane >= d) incl += v;
-    }
+    const int incl = wave_inclusive_scan(mine);
     const int all = __builtin_amdgcn_readlane(incl, kWave - 1);
-    const int64_t total = (int64_t)(all < a.tiles_m ? all : a.tiles_m) * a.tiles_n;
-    const int64_t id = xcd_order(block, total);
+    const int id = xcd_order(block, (all < a.tiles_m ? all : a.tiles_m) * a.tiles_n);
     if (id < 0) return false;
-    const int m = (int)(id / a.tiles_n);  // a row tile of the expert that holds the tile
+    const int m = (int)((unsigned)id / (unsigned)a.tiles_n);  // a row tile of the expert that holds the tile
     const int excl = incl - mine;
     const unsigned long long hit = __ballot(m >= excl && m < incl);
     if (!hit) return false;
@@ -486,11 +552,7 @@ __device__ __forceinline__ bool grouped_tile(const MatmulArgs &a, int BM, int bl
     at = __builtin_amdgcn_readlane(at, src);
     int4 r;
     if (fu < 0 || !group_record(a, fu, &r)) return false;
-    const int count = __builtin_amdgcn_readfirstlane(r.z);
-    const int nb = (count + BM - 1) / BM;
-    const int local = (int)(id - (int64_t)at * a.tiles_n);
-    *t = MatmulTile{__builtin_amdgcn_readfirstlane(r.x), __builtin_amdgcn_readfirstlane(r.y), count,
-                    (local % nb) * BM, local / nb, (int)id};
+    place(id, r, at);
     return true;
 }
 

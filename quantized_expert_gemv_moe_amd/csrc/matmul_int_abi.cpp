@@ -111,7 +111,7 @@ static bool choose_int_few(const moe_linear_int_t *L, const MatmulIntFewArgs &a,
     int cs = 0;
     int64_t tiles_n = 0;
     if (grouped) {
-        if (a.n_records > kIntFewRecords) return false;
+        if (a.n_records > kHeldRecords) return false;
         cs = 4;
         tiles_n = tiles(L->out_features, columns * cs);
         // more rows to a tile cost more than the launch

@@ -23,47 +23,16 @@ __device__ __forceinline__ void meet_lds() {
     meet();
 }
 
-// Row tile m of up to kIntFewRecords records, as grouped_tile finds it, but the record itself comes from the lane that has
-// loaded it (one trip to memory less ahead of the weights), and the grid's two dimensions take the place of
+// Row tile m of up to kHeldRecords records, as grouped_tile finds it, but the grid's two dimensions take the place of
 // divisions: a wave that has its SIMD to itself starts an instruction every 3 ns, so 300 of them on the way
 // are a microsecond.
 __device__ __forceinline__ bool few_grouped_tile(const MatmulArgs &a, int m, MatmulTile *t) {
-    constexpr int PER = kIntFewRecords / kWave;
-    const int lane = threadIdx.x & (kWave - 1);
-    int4 r[PER];
-    int tiles[PER], mine = 0;
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-        const int u = lane * PER + q;
-        r[q] = a.work[u < a.n_records ? u : 0];
-    }
-#pragma unroll
-    for (int q = 0; q < PER; ++q) {
-        const bool good = lane * PER + q < a.n_records && (unsigned)r[q].x < (unsigned)a.groups && r[q].y >= 0 && r[q].z >= 1 &&
-                          r[q].y <= a.rows - r[q].z;
-        tiles[q] = good ? (r[q].z + 15) / 16 : 0;
-        mine += tiles[q];
-    }
-    // records that overlap (malformed) may claim more than the grid holds: no lane's claim passes that
-    if (mine > a.tiles_m) mine = a.tiles_m;
-    const int incl = wave_inclusive_scan(mine);
-    int at = incl - mine;
-    const unsigned long long hit = __ballot(m >= at && m < incl);
-    if (!hit) return false;
-    const int src = __builtin_ctzll(hit);
-    int4 f = r[0];
-    int first = at;
-#pragma unroll
-    for (int q = 1; q < PER; ++q) {
-        at += tiles[q - 1];
-        const bool here = m >= at;
-        f.x = here ? r[q].x : f.x;
-        f.y = here ? r[q].y : f.y;
-        f.z = here ? r[q].z : f.z;
-        first = here ? at : first;
-    }
-    *t = MatmulTile{__builtin_amdgcn_readlane(f.x, src), __builtin_amdgcn_readlane(f.y, src),
-                    __builtin_amdgcn_readlane(f.z, src), (m - __builtin_amdgcn_readlane(first, src)) * 16, (int)blockIdx.x, 0};
+    HeldRecords h;
+    h.load(a, 16);
+    int4 r;
+    int before;
+    if (!h.find(m, &r, &before)) return false;
+    *t = MatmulTile{r.x, r.y, r.z, (m - before) * 16, (int)blockIdx.x, 0};
     return true;
 }
 

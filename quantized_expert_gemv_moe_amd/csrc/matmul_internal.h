@@ -42,9 +42,9 @@ struct MatmulIntArgs : MatmulArgs {
     int bias_dtype;                    // of bias and bias_up, either
 };
 
-// The kernel for few rows of an integer product, which takes x as it is given and finds its tile among up to so
-// many records.
-constexpr int kIntFewRecords = 256;
+constexpr int kHeldRecords = 256;  // of a plan, that a wave holds in registers while it looks for its tile
+
+// The kernel for few rows of an integer product, which takes x as it is given.
 struct MatmulIntFewArgs : MatmulIntArgs {
     const char *x_in;
     int64_t x_in_stride;             // bytes

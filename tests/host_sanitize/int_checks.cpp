@@ -68,7 +68,7 @@ static void try_call(const moe_linear_int_t &L, int32_t dtype, int64_t xs, int32
         EXPECT(c.tiles_m >= 1 && c.tiles_n >= 1 && (int64_t)c.tiles_m * c.tiles_n <= (int64_t)1 << 23);
         EXPECT(a.x_stride >= 0 && a.w_row > 0 && a.scale_group > 0 && a.n_records <= L.n_groups);
         if (c.kernel == kMatmulIntFew) {
-            EXPECT(dtype != MOE_DTYPE_I8 && q.rows == 0 && c.tiles_m <= 65535 && a.n_records <= kIntFewRecords);
+            EXPECT(dtype != MOE_DTYPE_I8 && q.rows == 0 && c.tiles_m <= 65535 && a.n_records <= kHeldRecords);
             EXPECT((int64_t)a.lds_rows * a.lds_stride <= 56 * 1024 && a.lds_stride >= a.K);
         }
         if (q.rows > 0) {
