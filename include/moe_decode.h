@@ -580,6 +580,7 @@ moe_status moe_router_check(const moe_router_t *router);
  *             moe_expert_plan, moe_decode_step and moe_combine take
  * Outputs must not overlap one another or the inputs.  A token's result depends on its
  * logits alone.  n_tokens == 0 returns MOE_OK without a launch.
+ * MOE_ERR_UNSUPPORTED for 2^26 tokens, 2^30 slots or strides past 2^32 elements and more.
  */
 moe_status moe_router_topk(const moe_router_t *router, const void *logits, int32_t logits_dtype,
                            int64_t logits_stride, int32_t n_tokens, int32_t *topk_idx, float *topk_w,

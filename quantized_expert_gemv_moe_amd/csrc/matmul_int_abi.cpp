@@ -159,7 +159,10 @@ moe_status prepare_matmul_int(const moe_linear_int_t *L, const void *x, int32_t 
     size_t used = 0;
     // Integers whose rows do not fill whole chunks at 16-byte addresses are copied into such rows where the weights' do: a
     // pass over x for the kernels of aligned rows (49216 rows, 1987 -> 704 into fp32: 316 us from where they are, 178 so).
-    // Few rows stay, and so do those that the caller's workspace has no room for.
+    // Few rows stay, and so do those that the caller's workspace has no room for.  us, from where they are and copied:
+    //   1003 -> 704   256 rows 10.6  9.8   1024 rows 10.7  9.8   2048 rows 12.9 10.8
+    //   1987 -> 2048  256 rows 10.9  9.8   512 rows  11.3 11.7   2048 rows 28.8 19.3
+    //   4099 -> 1024  256 rows 15.4 12.4   1024 rows 15.8 19.0   2048 rows 24.8 26.7
     bool copied = false;
     if (!own && rows > 0 && K >= 16 && linear_aligned(&view, L->row_tail) && x_rows >= kCopyRows &&
         (K % 16 || !aligned(x, 16) || stride_or(x_stride, K) % 16) && workspace && aligned(workspace, 256))

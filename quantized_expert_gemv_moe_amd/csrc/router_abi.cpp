@@ -24,7 +24,8 @@ moe_status prepare_router(const moe_router_t *r, const void *logits, int32_t dty
     if (st != MOE_OK) return st;
     if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_F16) return MOE_ERR_INVALID_ARG;
     if (n_tokens < 0 || stride < 0 || (stride && stride < r->n_experts)) return MOE_ERR_INVALID_ARG;
-    if ((int64_t)n_tokens * r->top_k > INT32_MAX / 2 || stride > (int64_t)1 << 32) return MOE_ERR_UNSUPPORTED;
+    // (a wave a token, and a launch has fewer than 2^32 threads)
+    if (n_tokens >= 1 << 26 || (int64_t)n_tokens * r->top_k > INT32_MAX / 2 || stride > (int64_t)1 << 32) return MOE_ERR_UNSUPPORTED;
     const int64_t es = (int64_t)dtype_size(dtype), row = stride ? stride : r->n_experts;
     if (n_tokens > ((int64_t)1 << 60) / (row * es)) return MOE_ERR_UNSUPPORTED;
     if (n_tokens > 0) {

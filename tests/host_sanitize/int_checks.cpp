@@ -188,6 +188,12 @@ static void router() {
                 EXPECT(st == MOE_OK || st == MOE_ERR_INVALID_ARG || st == MOE_ERR_UNSUPPORTED);
                 EXPECT(st != MOE_OK || (tokens >= 0 && dt >= 0 && dt <= 2 && stride >= 0));
             }
+    // a wave a token: one launch has fewer than 2^26 of them
+    for (int32_t tokens : {(1 << 26) - 1, 1 << 26, 1 << 28}) {
+        RouterArgs a;
+        EXPECT(prepare_router(&one, (const void *)kFar, MOE_DTYPE_F32, 0, tokens, (const int32_t *)(kFar * 2),
+                              (const float *)(kFar * 3), &a) == (tokens < 1 << 26 ? MOE_OK : MOE_ERR_UNSUPPORTED));
+    }
     for (float s : {0.f, -1.f, 1e-40f, 1.f, 3.4e38f, INFINITY, NAN}) {
         moe_router_t x = good;
         x.scale = s;
