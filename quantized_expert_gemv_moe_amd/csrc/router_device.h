@@ -279,9 +279,9 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
 }
 
 // ------------------------------------------------- four tokens a wave
-// Sixteen lanes a token, PL experts a lane, for up to 512 experts: most tokens are routed by 32-bit numbers with a proof that 64 bits would not choose otherwise,
-// the others (and those with masked experts or scores that are not numbers) by the whole wave
-// as above.
+// Sixteen lanes a token, PL experts a lane, for up to 512 experts: most tokens are routed by 32-bit numbers
+// with a proof that 64 bits would not choose otherwise, the others (and those with masked experts or
+// scores that are not numbers) by the whole wave as above.
 //
 // Key: where a value stands between the token's smallest and largest, in 22 bits, then 1023 - expert, so
 // that keys differ and a tie goes to the lower expert.  The mapping rises with the value, so keys
