@@ -400,7 +400,8 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
     }
     lo = row_reduce(lo, Min{});
     hi = row_reduce(hi, Max{});
-    clear = clear & (zero == 0.f);
+    // (values further apart than the largest number have no place between lo and hi: their keys mean nothing)
+    clear = clear & (zero == 0.f) & (hi - lo < INFINITY);
     // A sigmoid is off by at most 2.4e-7: its argument's product by |l| 2^-23, where s (1 - s) |l| < 0.23, its
     // exponential, sum and reciprocal by 1.5 steps.  A softmax score by 1.2e-6 of the largest: the same for the
     // exponentials, whose arguments' weighted mean is below ln 512.  And c by its addition's rounding, 2^-24 of it.
@@ -459,7 +460,7 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
 
     constexpr uint32_t kSteps = (1u << 22) - 8;
     float scale = (float)kSteps / (hi - lo);
-    scale = scale < 1e30f ? scale : 0.f;  // all alike (or not numbers): the check below has the last word
+    scale = scale < 1e30f ? scale : 0.f;  // all alike: the check below has the last word
     // experts out of the choice have 0 above their number, the others 1 and more
     const float by = kept ? scale : 0.f, from = kept ? 1.5f : 0.f;
     uint32_t key[PL];

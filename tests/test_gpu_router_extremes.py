@@ -1,0 +1,57 @@
+"""The scored router at the ends of its range, against its definition in 64 bits: values whose differences
+pass fp32's largest number (router_ref.py derives the tolerances)."""
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_expert_gemv_moe_amd as moe
+from gpu_helpers import log
+from test_gpu_router import DTYPES, compare, logits_of
+
+pytestmark = pytest.mark.gpu
+
+
+def spread(E, k, rng):
+    """Rows of both signs whose span passes fp32's largest number: one to all but one expert low, values alike and not."""
+    rows = []
+    for low in sorted({1, k - 1, k, k + 1, E // 2, E - k, E - 1} & set(range(1, E))):
+        for high_std, low_std in ((0.0, 0.0), (0.3, 0.0), (0.0, 0.3), (0.3, 0.3)):
+            v = 2e38 * (1 + high_std * rng.uniform(-1, 1, E))
+            at = rng.permutation(E)[:low]
+            v[at] = -2e38 * (1 + low_std * rng.uniform(-1, 1, low))
+            rows.append(v)
+    one = rng.standard_normal(E)
+    one[rng.integers(E)] = -3e38
+    other = one.copy()
+    other[(int(np.argmin(one)) + 1) % E] = 3e38
+    return np.array(rows + [one, other])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,keep", [(2, 1, 1), (24, 1, 1), (24, 4, 2), (64, 1, 1), (256, 8, 3), (512, 16, 5), (500, 1, 1),
+                                      (600, 1, 1), (640, 32, 7)])
+def test_logits_whose_span_passes_the_largest_number(E, G, keep, score, dtype):
+    log(f"[case] router span {E} {G} {keep} {score} {dtype}")
+    rng = np.random.default_rng(E + G)
+    for k in sorted({1, min(8, E // G * keep)}):
+        logits = torch.tensor(spread(E, k, rng), device="cuda").to(DTYPES[dtype])
+        assert bool(torch.isfinite(logits).all()) and bool((logits > torch.finfo(DTYPES[dtype]).min).all())
+        for by, renorm in (("max", True), ("top2", False)):
+            r = moe.Router(E, k, score=score, n_groups=G, top_groups=keep, group_score=by, renormalise=renorm)
+            compare(logits, dtype, r, f"span E={E} G={G} k={k} {by}")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,keep", [(2, 1, 1), (24, 4, 2), (256, 8, 3), (512, 16, 5), (600, 1, 1)])
+def test_biases_whose_span_passes_the_largest_number(E, G, keep, score):
+    log(f"[case] router bias span {E} {G} {keep} {score}")
+    rng = np.random.default_rng(E)
+    k = min(8, E // G * keep)
+    logits = logits_of(E, 6, E, "fp32")
+    for row in spread(E, k, rng):
+        bias = torch.tensor(row, dtype=torch.float32, device="cuda")
+        for by in ("max", "top2"):
+            r = moe.Router(E, k, score=score, bias=bias, n_groups=G, top_groups=keep, group_score=by)
+            compare(logits, "fp32", r, f"bias span E={E} G={G} {by}")
