@@ -434,6 +434,8 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
         if (a.seg >= 4) meet(Index<kXor2>{});
         if (a.seg >= 8) meet(Index<kHalfMirror>{});
         const float mine = a.top2 && a.per_group > 1 ? best + second : best;
+        // (two values whose sum passes the largest number have no order to one another)
+        clear = clear & (!live | (fabsf(mine) < INFINITY));
         const float over = !scores ? mine : mine + 4.f * delta, under = !scores ? mine : mine - 4.f * delta;
         // lanes whose group is surely, or maybe, before this one's; without margins lanes of equal
         // groups to the left as well

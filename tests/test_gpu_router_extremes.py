@@ -1,5 +1,5 @@
 """The scored router at the ends of its range, against its definition in 64 bits: values whose differences
-pass fp32's largest number (router_ref.py derives the tolerances)."""
+or sums pass fp32's largest number (router_ref.py derives the tolerances)."""
 
 import numpy as np
 import pytest
@@ -55,3 +55,23 @@ def test_biases_whose_span_passes_the_largest_number(E, G, keep, score):
         for by in ("max", "top2"):
             r = moe.Router(E, k, score=score, bias=bias, n_groups=G, top_groups=keep, group_score=by)
             compare(logits, "fp32", r, f"bias span E={E} G={G} {by}")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_groups_whose_sums_pass_the_largest_number(score):
+    """Sums of two biases that fp32 holds and fp32 would make infinite, of either sign: groups in the order of the sums."""
+    log(f"[case] router group sums {score}")
+    pairs = {(2, 1): [[0, 0], [3.3e38, 0.3e38], [2.5e38, 2.5e38], [0, 0]],
+             (2, 2): [[1.8e38, 1.7e38], [3.3e38, 0.3e38], [2.5e38, 2.5e38], [3.4e38, 3.4e38]],
+             (2, 3): [[-3e38, -3e38], [-2e38, -2e38], [-3.2e38, -1e38], [-2.5e38, -2.5e38]]}
+    for (per, keep), groups in pairs.items():
+        for order in ((0, 1, 2, 3), (2, 1, 3, 0), (3, 2, 1, 0)):
+            for wide in (1, 3, 16):  # two of a group's experts, the others far below
+                bias = torch.full((4, per * wide), -3.3e38, device="cuda")
+                for g, o in enumerate(order):
+                    bias[g, [0, per * wide - 1]] = torch.tensor(groups[o], device="cuda")
+                bias = bias.view(-1).contiguous()
+                E = bias.numel()
+                for k in {1, min(8, per * wide * keep)}:
+                    r = moe.Router(E, k, score=score, bias=bias, n_groups=4, top_groups=keep, group_score="top2")
+                    compare(logits_of(E, 5, E, "fp32"), "fp32", r, f"sums {order} E={E} keep={keep} k={k}")
