@@ -69,7 +69,7 @@ def test_groups_whose_sums_pass_the_largest_number(score):
             for wide in (1, 3, 16):  # two of a group's experts, the others far below
                 bias = torch.full((4, per * wide), -3.3e38, device="cuda")
                 for g, o in enumerate(order):
-                    bias[g, [0, per * wide - 1]] = torch.tensor(groups[o], device="cuda")
+                    bias[g, [0, per * wide - 1]] = torch.tensor(groups[o], dtype=torch.float32, device="cuda")
                 bias = bias.view(-1).contiguous()
                 E = bias.numel()
                 for k in {1, min(8, per * wide * keep)}:
