@@ -543,7 +543,8 @@ typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
  *   s = softmax(l) over all experts, or sigmoid(l)
  *   c = s + bias, in 64 bits.  Without a bias experts are in the order of l itself,
  *       in which s rises.  Scores below 1e-300 (a sigmoid of l < -690) may count
- *       as zero.
+ *       as zero, but not for the weights of a renormalised softmax: those are the softmax of
+ *       the chosen logits, however far an expert that is not chosen is above them.
  * An expert is masked when its logit is -infinity or the lowest finite value of the logits'
  * type, or its bias is -infinity.  The softmax leaves out experts masked by their logits.
  *   Of n_groups groups of n_experts / n_groups consecutive experts the top_groups best are

@@ -47,7 +47,8 @@ __device__ __forceinline__ double exp64(double x) {
     p = fma(p, r, 1.0);
     return ldexp(p, (int)n);
 }
-// 1 / d, d >= 0, by two steps of Newton's method; 0 from 1e300 on.
+// 1 / d, d at least 2^-1022 (below it the first step is infinite and the next NaN), by two steps of Newton's
+// method; 0 from 1e300 on.
 __device__ __forceinline__ double rcp64(double d) {
     double r = __builtin_amdgcn_rcp(d);
     r = fma(fma(-d, r, 1.0), r, r);
@@ -267,7 +268,8 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
 
     // weights of the chosen, lanes 0 .. top_k - 1
     const bool mine = lane < a.top_k && !my_mask;
-    if (!a.sigmoid && !all_scores) top = wave_max(mine ? my_l : -INFINITY);
+    // renormalised: against the largest of them, so that their sum is 1 and more, however far the others are above
+    if (!a.sigmoid && a.renormalise) top = wave_max(mine ? my_l : -INFINITY);
     // (one pass over the wave for all of them: 64 bits cost nothing here)
     double v = exp64(a.sigmoid ? -(double)my_l : (double)my_l - (double)top);
     v = a.sigmoid ? rcp64(1.0 + v) : v;
@@ -534,7 +536,7 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
     }
     clear = clear & gaps;
 
-    if (!a.sigmoid && a.renormalise && !scores) top = row_reduce(chosen ? my_l : kNone, Max{});
+    if (!a.sigmoid && a.renormalise) top = row_reduce(chosen ? my_l : kNone, Max{});
     double v = exp64(a.sigmoid ? -(double)my_l : (double)my_l - (double)top);
     if (a.sigmoid) v = rcp64(1.0 + v);
     v = chosen ? v : 0.0;

@@ -1,5 +1,6 @@
 """The scored router at the ends of its range, against its definition in 64 bits: values whose differences
-or sums pass fp32's largest number (router_ref.py derives the tolerances)."""
+or sums pass fp32's largest number, and chosen experts far below the others (router_ref.py derives the
+tolerances)."""
 
 import numpy as np
 import pytest
@@ -75,3 +76,33 @@ def test_groups_whose_sums_pass_the_largest_number(score):
                 for k in {1, min(8, per * wide * keep)}:
                     r = moe.Router(E, k, score=score, bias=bias, n_groups=4, top_groups=keep, group_score="top2")
                     compare(logits_of(E, 5, E, "fp32"), "fp32", r, f"sums {order} E={E} keep={keep} k={k}")
+
+
+@pytest.mark.parametrize("low", [0.0, -712.0, -730.0, -744.0, -800.0, -1e5, -2e38])
+@pytest.mark.parametrize("E,G", [(64, 1), (256, 8), (600, 1), (640, 32)])
+def test_renormalised_softmax_far_below_the_largest_logit(E, G, low):
+    """The chosen experts' weights are the softmax of their own logits, however far an expert that the bias leaves out is
+    above them, and whether 32 bits or the whole wave settle the token."""
+    log(f"[case] router far below {E} {G} {low}")
+    k, chosen = 6, np.arange(3, 9) + E // 2
+    logits = np.full((5, E), low)
+    steps = np.array([0.0, -0.5, -1.25, 0.75, -3.0, 0.25])
+    logits[:, chosen] += steps * max(1.0, abs(low) * 2.0 ** -20)  # (a step that fp32 holds next to low)
+    logits[:, 0] = 0.0
+    logits[2, 1] = -np.inf                    # a masked one: the whole wave's way
+    logits[3, chosen] = low                   # all alike
+    logits[4, chosen[2]] = min(low * 1.1, low - 30.0)
+    bias = torch.zeros(E, device="cuda")
+    bias[torch.as_tensor(chosen)] = 2.0 + torch.arange(k, 0, -1, device="cuda") * 0.5
+    lg = torch.tensor(logits, dtype=torch.float32, device="cuda")
+    for by, scale in (("max", 1.0), ("top2", 2.5)):
+        r = moe.Router(E, k, bias=bias, n_groups=G, top_groups=1, group_score=by, scale=scale)
+        idx, w = moe.router_topk(r, lg)
+        torch.cuda.synchronize()
+        assert idx.cpu().tolist() == [chosen.tolist()] * 5
+        l = lg.double().cpu().numpy()[:, chosen]
+        e = np.exp(l - l.max(axis=1, keepdims=True))
+        want = e / e.sum(axis=1, keepdims=True) * scale
+        # 64 bits, 2^-48 of exponentials, sum and quotient, then one rounding to fp32
+        off = np.abs(w.double().cpu().numpy() - want)
+        assert (off <= want * (2.0 ** -24 + 2.0 ** -48) + 2.0 ** -150).all(), f"{by}: {w.cpu()} for {want}"
