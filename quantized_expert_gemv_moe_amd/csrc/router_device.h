@@ -295,7 +295,8 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
 // is taken out.  One more round than top_k shows that the last choice is clear as well.  Where choices
 // are not clear, sixteen of them are put in the order of their 64-bit values (some 4 tokens of 8192); the
 // whole wave's way, for what is then still open, takes 5 us longer: a wave alone on its SIMD starts an
-// instruction every 3 ns.
+// instruction every 3 ns.  Open choices of a biased softmax go there at once, as its scores need the sum over all
+// experts in 64 bits (8192 tokens of 256 experts 10.9 us; 24.0 with the three tokens beside an open one taken along).
 //
 // What bounds it: the instructions, some 200 a token of 256 experts.  8192 tokens of 256 experts, biased
 // and grouped: 20.2 us with a wave a token in 64 bits throughout, 7.3 so; 16384 of 128, plain:
@@ -510,29 +511,37 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
         // (what stands behind the last one looked at may have its place too)
         gaps = !pair | (gap > 0) | ((my_l >= l_next) & (r < a.top_k - 1));
     }
-    if (__ballot(!gaps & clear)) {
+    // (a biased softmax score takes the sum of all experts in 64 bits: the whole wave's way)
+    const unsigned long long open = !BIAS || a.sigmoid ? __ballot(!gaps & clear) : 0;
+    if (open) {
         // Up to sixteen candidates in the order of their exact values: right if what was not looked at is
-        // clearly less than the last one chosen.
+        // clearly less than the last one chosen.  Only open tokens take it: a token's result, to the last bit of
+        // its weights, must not depend on the three beside it.
+        const bool mine = (open >> row0) & 0xFFFF;
         const int total = all < 16 ? all : 16;
         choose(total);
-        e = r < total ? expert(my_key) : 0;
-        load_lane<1>(a.logits, at + e, 1, false, a.dtype, &my_l);
-        double exact = (double)my_l;
-        if constexpr (BIAS) exact = sigmoid64(exact) + (double)a.bias[e];
+        int e16 = r < total ? expert(my_key) : 0;
+        float l16;
+        load_lane<1>(a.logits, at + e16, 1, false, a.dtype, &l16);
+        double exact = (double)l16;
+        if constexpr (BIAS) exact = sigmoid64(exact) + (double)a.bias[e16];
         if (r >= total) exact = kNone;
         int before = 0;
         static_for<15>([&](auto i) __attribute__((always_inline)) {
             constexpr int kRor = 0x121 + decltype(i)::value;
             const double other = row_move64<kRor>(exact);
-            before += (other > exact) | ((other == exact) & (row_move<kRor>(e) < e));
+            before += (other > exact) | ((other == exact) & (row_move<kRor>(e16) < e16));
         });
         before = r < total ? before : r;
         const int to = (row0 + before) * 4;
-        e = __builtin_amdgcn_ds_permute(to, e);
-        my_l = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(my_l)));
+        e16 = __builtin_amdgcn_ds_permute(to, e16);
+        l16 = __int_as_float(__builtin_amdgcn_ds_permute(to, __float_as_int(l16)));
         const uint32_t placed = (uint32_t)__builtin_amdgcn_ds_permute(to, (int)my_key);
-        gaps = (!BIAS || a.sigmoid) &
-               ((r != a.top_k - 1) | (total == all) | (((float)((placed >> 10) - (m >> 10)) > far) & (a.top_k < total)));
+        const bool settled =
+            (r != a.top_k - 1) | (total == all) | (((float)((placed >> 10) - (m >> 10)) > far) & (a.top_k < total));
+        e = mine ? e16 : e;
+        my_l = mine ? l16 : my_l;
+        gaps = mine ? settled : gaps;
     }
     clear = clear & gaps;
 

@@ -1,6 +1,6 @@
 """The scored router at the ends of its range, against its definition in 64 bits: values whose differences
-or sums pass fp32's largest number, and chosen experts far below the others (router_ref.py derives the
-tolerances)."""
+or sums pass fp32's largest number, chosen experts far below the others, and tokens next to ones whose
+order 32 bits leave open (router_ref.py derives the tolerances)."""
 
 import numpy as np
 import pytest
@@ -8,7 +8,7 @@ import torch
 
 import quantized_expert_gemv_moe_amd as moe
 from gpu_helpers import log
-from test_gpu_router import DTYPES, compare, logits_of
+from test_gpu_router import DTYPES, compare, gen, logits_of
 
 pytestmark = pytest.mark.gpu
 
@@ -106,3 +106,34 @@ def test_renormalised_softmax_far_below_the_largest_logit(E, G, low):
         # 64 bits, 2^-48 of exponentials, sum and quotient, then one rounding to fp32
         off = np.abs(w.double().cpu().numpy() - want)
         assert (off <= want * (2.0 ** -24 + 2.0 ** -48) + 2.0 ** -150).all(), f"{by}: {w.cpu()} for {want}"
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True], ids=["plain", "biased"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_a_token_does_not_notice_its_neighbours(renorm, biased, score):
+    """The same bits whether a token is alone, next to ordinary tokens or next to ones that 32 bits cannot order, and
+    from either entry point."""
+    log(f"[case] router neighbours renorm={renorm} biased={biased} {score}")
+    for E, G, keep in ((64, 1, 1), (256, 8, 4), (512, 16, 3)):
+        T = 400
+        logits = logits_of(E, T, E, "fp32", 2.0)
+        bias = torch.empty(E, device="cuda").normal_(0.0, 0.1, generator=gen(1)) if biased else None
+        if biased:
+            bias[5] = bias[9] = 3.0  # two that are chosen, in an order that equal scores leave to their ids
+        r = moe.Router(E, 8, score=score, bias=bias, n_groups=G, top_groups=keep, group_score="top2", renormalise=renorm)
+        alone = [moe.router_topk(r, logits[t:t + 1]) for t in range(T)]
+        idx, w = torch.cat([a[0] for a in alone]), torch.cat([a[1] for a in alone])
+        for every in (2, 3, 4):
+            mixed = logits.clone()
+            mixed[::every] = 0.0                # all alike: open to the end
+            mixed[::every, 9] = mixed[::every, 5] = 4.0
+            got = moe.router_topk(r, mixed)
+            plan = moe.router_plan(r, mixed[:64])
+            torch.cuda.synchronize()
+            keeps = torch.arange(T, device="cuda") % every != 0
+            for i, ww in ((got[0], got[1]), (torch.cat([plan[0], got[0][64:]]), torch.cat([plan[1], got[1][64:]]))):
+                assert torch.equal(i[keeps], idx[keeps])
+                off = (ww[keeps].view(torch.int32) != w[keeps].view(torch.int32)).sum().item()
+                assert off == 0, f"E={E} every={every}: {off} weights differ"
+        compare(mixed, "fp32", r, f"neighbours E={E}")
