@@ -406,8 +406,12 @@ __device__ __forceinline__ void router_four(const RouterArgs &a, const RouterArg
     // (values further apart than the largest number have no place between lo and hi: their keys mean nothing)
     clear = clear & (zero == 0.f) & (hi - lo < INFINITY);
     // A sigmoid is off by at most 2.4e-7: its argument's product by |l| 2^-23, where s (1 - s) |l| < 0.23, its
-    // exponential, sum and reciprocal by 1.5 steps.  A softmax score by 1.2e-6 of the largest: the same for the
-    // exponentials, whose arguments' weighted mean is below ln 512.  And c by its addition's rounding, 2^-24 of it.
+    // exponential, sum and reciprocal by 1.5 steps.  A softmax score by 49 steps of 2^-24 of the largest, 2.9e-6, for which
+    // 64 are taken: 2.4 of its own exponential (of the argument x e^-x < 0.37, of the function 2), and of the total's
+    // 6.2 of the arguments (their weighted mean is below ln 512), 2 of the functions, PL - 1 and 4 of the additions
+    // in a lane and over the lanes, 2 of the reciprocal and 1 of the product.  And c by its addition's rounding,
+    // 2^-24 of it.
+    static_assert(PL <= 32, "delta counts 31 additions in a lane");
     const float delta = (a.sigmoid ? 0x1p-21f : 0x1p-18f * largest) + 0x1p-23f * fmaxf(fabsf(lo), fabsf(hi));
 
     bool kept = live;
