@@ -660,7 +660,9 @@ size_t moe_grouped_int_workspace_size(const moe_linear_int_t *linear, int32_t ma
  *             x_dtype fp32, bf16 or fp16: quantised within the call; x_scale is NULL
  *   workspace moe_matmul_int_workspace_size(linear, n_rows) bytes, 256-byte aligned; contents
  *             need no initialisation.  Calls that may overlap in time need one each.
- *             A call that needs less takes less (none: NULL will do).
+ *             x of a floating type asks for all of it, whether the call's kernel writes to it or
+ *             not.  x of integers takes less: NULL where K is not split, and without room for
+ *             a copy rows that are no whole chunks are read where they are.
  * The integer sum is exact; it, the two scales' product and their product are rounded to
  * fp32 once each, what follows is as in moe_matmul.  Repeated calls are bitwise equal.
  */
