@@ -663,8 +663,10 @@ size_t moe_grouped_int_workspace_size(const moe_linear_int_t *linear, int32_t ma
  *             x of a floating type asks for all of it, whether the call's kernel writes to it or
  *             not.  x of integers takes less: NULL where K is not split, and without room for
  *             a copy rows that are no whole chunks are read where they are.
- * The integer sum is exact; it, the two scales' product and their product are rounded to
- * fp32 once each, what follows is as in moe_matmul.  Repeated calls are bitwise equal.
+ * The integer sum is exact; it and the two scales' product are rounded to fp32 once each, and so is
+ * what their product and the bias come to (a fused multiply-add).  What follows is as in moe_matmul;
+ * the last product, of f or of the gate, and a residual's sum may be rounded together.  Repeated
+ * calls are bitwise equal.
  */
 moe_status moe_matmul_int(const moe_linear_int_t *linear, const void *x, int32_t x_dtype, int64_t x_stride,
                          const float *x_scale, int32_t n_rows, const void *residual, int32_t residual_dtype,

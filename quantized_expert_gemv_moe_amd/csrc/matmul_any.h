@@ -115,8 +115,8 @@ __global__ __launch_bounds__(256) void matmul_tile64_kernel(Args<DT> a) {
     load_scales<DT, GATED, NT>(a, t.group, col, sc);
     static_for<MT>([&](auto m) {
         const int o = orow[wm * 32 + m * 16 + r16];
-        scale_row<DT, NT>(acc[m], sc, x_factor<DT>(a, o));
-        finish_row<GATED, NT>(a, o, col, acc[m], b);
+        add_bias<DT, NT>(acc[m], sc, x_factor<DT>(a, o), b);
+        finish_row<GATED, NT>(a, o, col, acc[m]);
     });
 }
 

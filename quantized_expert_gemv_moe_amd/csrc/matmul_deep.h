@@ -238,8 +238,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void matmul_deep_kernel(Args<DT> a
     load_bias<DT, GATED, NT>(a, t.group, col, b);
     static_for<MT>([&](auto m) {
         const int o = orow[wm * 16 * MT + m * 16 + r16];
-        scale_row<DT, NT>(acc[m], sc, xf[m]);
-        finish_row<GATED, NT>(a, o, col, acc[m], b);
+        add_bias<DT, NT>(acc[m], sc, xf[m], b);
+        finish_row<GATED, NT>(a, o, col, acc[m]);
     });
 }
 

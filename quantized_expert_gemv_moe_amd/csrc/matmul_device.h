@@ -39,7 +39,7 @@ template <int DT>
 using Args = typename ArgsOf<DT>::type;
 
 // One 64-byte step of a 16 x 16 tile.  Accumulators are mm_f32x4 for every type; those of
-// integer products hold the bits of 32-bit integers until scale_row widens them.
+// integer products hold the bits of 32-bit integers until add_bias widens them.
 template <int DT>
 __device__ __forceinline__ mm_f32x4 mma(const mm_u32x4 &a, const mm_u32x4 &b, mm_f32x4 c) {
     if constexpr (DT == MOE_DTYPE_BF16) {
@@ -242,7 +242,7 @@ __device__ __forceinline__ void store_row(const MatmulArgs &a, int o, int col, c
 // as fp32 evaluates it): a least-squares fit at 4000 Chebyshev nodes of t,
 // weighted by t / g, made for this file from 64-bit values of g.  The tail keeps its relative accuracy, which
 // 0.5 (1 + erf) would lose.
-__device__ __forceinline__ float gelu_normal(float z) {
+__device__ __forceinline__ float normal_factor(float z) {  // Phi(z)
     const float a = fabsf(z) * 0.70710678118654752f;
     const float t = __builtin_amdgcn_rcpf(fmaf(0.5f, a, 1.0f));
     float p = -0.0601087077f;
@@ -255,25 +255,55 @@ __device__ __forceinline__ float gelu_normal(float z) {
     p = fmaf(p, t, 0.282453842f);
     p = fmaf(p, t, 0.282082358f);
     const float tail = 0.5f * p * t * expf(-0.5f * z * z);  // erfc(a) / 2
-    return z * (z > 0.f ? 1.0f - tail : tail);
+    return z > 0.f ? 1.0f - tail : tail;
 }
+__device__ __forceinline__ float gelu_normal(float z) { return z * normal_factor(z); }
 
 __device__ __forceinline__ float clip(float z, float limit) {  // NaN stays NaN
     return z > limit ? limit : (z < -limit ? -limit : z);
 }
 
-// z / (1 + exp(-a)).  The exponential is 2 to the rounded product -a log2(e): off by |a|
+// 1 / (1 + exp(-a)).  The exponential is 2 to the rounded product -a log2(e): off by |a|
 // 2^-24 relative where it counts, which is below the rounding of 16-bit outputs and
 // next to that of the products' sums in fp32.  The reciprocal is good to 1 ulp; below
 // 2^-126 it is zero, so f counts as zero from a = -87.3 down (1e-36 and less).
-__device__ __forceinline__ float sigmoid_mul(float z, float a) {
-    return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.4426950408889634f));
+__device__ __forceinline__ float sigmoid_factor(float a) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.4426950408889634f));
 }
+__device__ __forceinline__ float sigmoid_mul(float z, float a) { return z * sigmoid_factor(a); }
 __device__ __forceinline__ float silu(float z) { return sigmoid_mul(z, z); }
 // 0.5 (1 + tanh(b)) = 1 / (1 + exp(-2 b)): no cancellation
-__device__ __forceinline__ float gelu_tanh(float z) {
-    return sigmoid_mul(z, 1.5957691216057308f * (z + 0.044715f * z * z * z));
+__device__ __forceinline__ float tanh_factor(float z) {
+    return sigmoid_factor(1.5957691216057308f * (z + 0.044715f * z * z * z));
 }
+__device__ __forceinline__ float gelu_tanh(float z) { return z * tanh_factor(z); }
+
+// The functions as f(z) = pre(z) factor(pre(z)), for a last product that is rounded with the sum behind it.
+struct FnNone {
+    static __device__ __forceinline__ float pre(float z) { return z; }
+    static __device__ __forceinline__ float factor(float) { return 1.f; }
+    __device__ __forceinline__ float operator()(float z) const { return z; }
+};
+struct FnRelu {
+    static __device__ __forceinline__ float pre(float z) { return z < 0.f ? 0.f : z; }
+    static __device__ __forceinline__ float factor(float) { return 1.f; }
+    __device__ __forceinline__ float operator()(float z) const { return pre(z); }
+};
+struct FnSilu {
+    static __device__ __forceinline__ float pre(float z) { return z; }
+    static __device__ __forceinline__ float factor(float z) { return sigmoid_factor(z); }
+    __device__ __forceinline__ float operator()(float z) const { return silu(z); }
+};
+struct FnGelu {
+    static __device__ __forceinline__ float pre(float z) { return z; }
+    static __device__ __forceinline__ float factor(float z) { return normal_factor(z); }
+    __device__ __forceinline__ float operator()(float z) const { return gelu_normal(z); }
+};
+struct FnGeluTanh {
+    static __device__ __forceinline__ float pre(float z) { return z; }
+    static __device__ __forceinline__ float factor(float z) { return tanh_factor(z); }
+    __device__ __forceinline__ float operator()(float z) const { return gelu_tanh(z); }
+};
 
 // f over N accumulators.  The function is uniform over the launch, so the choice
 // is made once for all of them and not per element.
@@ -311,14 +341,12 @@ __device__ __forceinline__ void static_for(F &&f) {
     }
 }
 
-// A row's accumulators to its stored values: bias, clip, f, gate, residual, one
+// A row's accumulators behind add_bias to its stored values: clip, f, gate, residual, one
 // rounding.  The lane's first column is col; gate is in the first NC accumulators and
-// up in the others when gated.  b holds the columns' biases.
+// up in the others when gated.
 template <bool GATED, int NT>
-__device__ __forceinline__ void finish_row(const MatmulArgs &a, int o, int col, mm_f32x4 *z, const mm_f32x4 *b) {
+__device__ __forceinline__ void finish_row(const MatmulArgs &a, int o, int col, mm_f32x4 *z) {
     constexpr int NC = GATED ? NT / 2 : NT;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) z[n] += b[n];
     if (a.clamp > 0.f) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -369,8 +397,7 @@ __device__ __forceinline__ void load_bias(const Args<DT> &a, int group, int col,
 }
 
 // What a lane's integer products are scaled with: a factor for each of its columns, as load_bias
-// has them, and one for the row.  A row's sum is rounded to fp32 once, the two factors'
-// product once and theirs once.  Nothing of it exists for the other types.
+// has them, and one for the row.  Nothing of it exists for the other types.
 template <int DT, bool GATED, int NT, bool WHOLE = false>
 __device__ __forceinline__ void load_scales(const Args<DT> &a, int group, int col, mm_f32x4 *sc) {
     if constexpr (DT == MOE_DTYPE_I8) {
@@ -390,13 +417,19 @@ __device__ __forceinline__ void load_scales(const Args<DT> &a, int group, int co
         }
     }
 }
+// A row's accumulators with their biases b.  Of an integer product the sum is rounded to fp32 once, the
+// two factors' product once, and their product with the bias once: a fused multiply-add in so many words, as
+// a compiler would fuse a product and a sum in one place and not in another.
 template <int DT, int NT>
-__device__ __forceinline__ void scale_row(mm_f32x4 *z, const mm_f32x4 *sc, float row) {
-    if constexpr (DT == MOE_DTYPE_I8) {
+__device__ __forceinline__ void add_bias(mm_f32x4 *z, const mm_f32x4 *sc, float row, const mm_f32x4 *b) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        if constexpr (DT == MOE_DTYPE_I8) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) z[n][r] = (float)__float_as_int(z[n][r]) * (row * sc[n][r]);
+            for (int r = 0; r < 4; ++r) z[n][r] = fmaf((float)__float_as_int(z[n][r]), row * sc[n][r], b[n][r]);
+        } else {
+            z[n] += b[n];
+        }
     }
 }
 

@@ -121,8 +121,8 @@ __global__ __launch_bounds__(512, RT == 1 ? 4 : 2) void matmul_few_kernel(Args<D
             if constexpr (GATED && !PAIR) z[1] = sum(1, lane);
             load_bias<DT, GATED, GATED ? 2 : 1>(a, 0, col0 + 4 * g, b);
             load_scales<DT, GATED, GATED ? 2 : 1>(a, 0, col0 + 4 * g, sc);
-            scale_row<DT, GATED ? 2 : 1>(z, sc, x_factor<DT>(a, orow[m]));
-            finish_row<GATED, GATED ? 2 : 1>(a, PAIR && g >= 2 ? -1 : orow[m], col0 + 4 * g, z, b);
+            add_bias<DT, GATED ? 2 : 1>(z, sc, x_factor<DT>(a, orow[m]), b);
+            finish_row<GATED, GATED ? 2 : 1>(a, PAIR && g >= 2 ? -1 : orow[m], col0 + 4 * g, z);
         }
     });
 }

@@ -186,8 +186,8 @@ __global__ __launch_bounds__(512) void matmul_int_few_kernel(MatmulIntFewArgs a)
     z[0] = sum(lane);
     if constexpr (GATED) z[1] = sum((lane + 32) & 63);
     load_bias<MOE_DTYPE_I8, GATED, NT>(a, t.group, c4, b);
-    scale_row<MOE_DTYPE_I8, NT>(z, sc, factor[r16 < rows ? r16 : 0]);
-    finish_row<GATED, NT>(a, r16 < rows && !(GATED && g >= 2) ? orow[r16] : -1, c4, z, b);
+    add_bias<MOE_DTYPE_I8, NT>(z, sc, factor[r16 < rows ? r16 : 0], b);
+    finish_row<GATED, NT>(a, r16 < rows && !(GATED && g >= 2) ? orow[r16] : -1, c4, z);
 }
 
 template <int XT, bool GATED>

@@ -106,7 +106,8 @@ __global__ __launch_bounds__(256, DT == MOE_DTYPE_I8 && MT * NT < 64 ? 2 : 1) vo
     const int g = lane >> 4, r16 = lane & 15;
     int col0 = t.tile_n * 2 * CW;
     // The last columns of an integer product: the last whole tile of them, so that they have the straight path as well.
-    // What the tile before has of them is computed twice, to the same bits (not where out is the
+    // What the tile before has of them is computed twice, to the same bits: sums are exact, and the straight path has
+    // every rounding in so many words (not where out is the
     // residual, which the first of the two would have changed).  4096 x 4096 x 4000: 67.5 us in the loop, 51.6 so.
     if (DT == MOE_DTYPE_I8 && a.N >= 2 * CW && (!a.residual || (a.residual != a.out && a.res_dtype == a.out_dtype)))
         col0 = col0 < a.N - 2 * CW ? col0 : a.N - 2 * CW;
@@ -311,15 +312,22 @@ __global__ __launch_bounds__(256, DT == MOE_DTYPE_I8 && MT * NT < 64 ? 2 : 1) vo
                                 res[m % 2][n / 2][k] = load_whole<OT, !INT>((const char *)(p + acc_col<NTC>(n) + 4 * k));
                     }
                 };
+                auto residual = [&](int m, int n, int i) __attribute__((always_inline)) -> float {
+                    if constexpr (OT == MOE_DTYPE_F32) {
+                        return __uint_as_float(res[m % 2][n / 2][i / 4][i % 4]);
+                    } else {
+                        const uint32_t w = res[m % 2][n / 2][0][i / 2];
+                        const uint16_t h = (uint16_t)(i % 2 ? w >> 16 : w);
+                        return OT == MOE_DTYPE_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+                    }
+                };
                 fetch(Index<0>{});
                 static_for<MT>([&](auto m) __attribute__((always_inline)) {
                     __builtin_amdgcn_sched_barrier(0);  // all rows together would not fit the registers
                     if constexpr (m + 1 < MT) fetch(Index<m + 1>{});
                     mm_f32x4 *z = acc[m];
                     if constexpr (ACC) hold<NT, m == MT - 1>(z);
-                    scale_row<DT, NT>(z, sc, xf[m]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) z[n] += b[n];
+                    add_bias<DT, NT>(z, sc, xf[m], b);
                     if (a.clamp > 0.f) {
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
@@ -333,16 +341,24 @@ __global__ __launch_bounds__(256, DT == MOE_DTYPE_I8 && MT * NT < 64 ? 2 : 1) vo
                         float v[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            v[i] = f(z[n + i / 4][i % 4]);
-                            if constexpr (GATED) v[i] *= z[n + NTC + i / 4][i % 4];
-                            if constexpr (has_residual) {
-                                if constexpr (OT == MOE_DTYPE_F32) {
-                                    v[i] += __uint_as_float(res[m % 2][n / 2][i / 4][i % 4]);
+                            const float z0 = z[n + i / 4][i % 4];
+                            if constexpr (INT) {  // the last product and the residual's sum are rounded together
+                                const float p = f.pre(z0), q = f.factor(p);
+                                const float up = GATED ? z[(n + NTC + i / 4) % NT][i % 4] : 1.f;
+                                const float a0 = GATED ? p * q : p, b0 = GATED ? up : q;
+                                if constexpr (has_residual) {
+                                    v[i] = fmaf(a0, b0, residual(m, n, i));
+                                    // The compiler has an instruction that rounds such a sum straight to fp16, and takes it
+                                    // in some places of a tile and not in others: some of the values that two tiles
+                                    // write differed.
+                                    if constexpr (OT == MOE_DTYPE_F16) asm("" : "+v"(v[i]));
                                 } else {
-                                    const uint32_t w = res[m % 2][n / 2][0][i / 2];
-                                    const uint16_t h = (uint16_t)(i % 2 ? w >> 16 : w);
-                                    v[i] += OT == MOE_DTYPE_BF16 ? bf16_bits_to_f32(h) : f16_bits_to_f32(h);
+                                    v[i] = a0 * b0;
                                 }
+                            } else {
+                                v[i] = f(z0);
+                                if constexpr (GATED) v[i] *= z[n + NTC + i / 4][i % 4];
+                                if constexpr (has_residual) v[i] += residual(m, n, i);
                             }
                         }
                         if constexpr (OT == MOE_DTYPE_F32) {
@@ -379,19 +395,19 @@ __global__ __launch_bounds__(256, DT == MOE_DTYPE_I8 && MT * NT < 64 ? 2 : 1) vo
             switch (a.fn) {
                 case MOE_FN_NONE:
                     if constexpr (INT && GATED) break;  // as good as never gated
-                    either([](float z) { return z; });
+                    either(FnNone{});
                     return;
-                case MOE_FN_SILU: either([](float z) { return silu(z); }); return;
-                case MOE_FN_GELU_TANH: either([](float z) { return gelu_tanh(z); }); return;
+                case MOE_FN_SILU: either(FnSilu{}); return;
+                case MOE_FN_GELU_TANH: either(FnGeluTanh{}); return;
                 case MOE_FN_GELU:
                     if constexpr (INT) {
-                        either([](float z) { return gelu_normal(z); });
+                        either(FnGelu{});
                         return;
                     }
                     break;
                 case MOE_FN_RELU:
                     if constexpr (INT && !GATED) {
-                        either([](float z) { return z < 0.f ? 0.f : z; });
+                        either(FnRelu{});
                         return;
                     }
                     break;
@@ -443,11 +459,11 @@ __global__ __launch_bounds__(256, DT == MOE_DTYPE_I8 && MT * NT < 64 ? 2 : 1) vo
                     sc[u] = col_factor[u][(c - col0) / 4];
                     b[u] = col_bias[u][(c - col0) / 4];
                 }
-                scale_row<DT, GATED ? 2 : 1>(z, sc, row_factor[row]);
             } else {
                 load_bias<DT, GATED, GATED ? 2 : 1>(a, t.group, c, b);
             }
-            finish_row<GATED, GATED ? 2 : 1>(a, o, c, z, b);
+            add_bias<DT, GATED ? 2 : 1>(z, sc, DT == MOE_DTYPE_I8 ? row_factor[row] : 1.f, b);
+            finish_row<GATED, GATED ? 2 : 1>(a, o, c, z);
         }
     });
 }
