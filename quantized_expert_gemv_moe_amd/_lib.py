@@ -1062,6 +1062,8 @@ class LinearInt:
             raise ValueError(f"activation must be one of {sorted(_FNS)}")
         if clamp_limit > 0 and C.c_float(clamp_limit).value == 0:
             raise ValueError("clamp_limit is too small for fp32, where it would be zero and mean none")
+        if w_scale is None:
+            raise ValueError("w_scale is needed: fp32 [out] or [experts, out]")
         if w is None or w.dim() not in (2, 3) or w.dtype is not torch.int8 or not w.is_cuda or w.numel() == 0:
             raise ValueError("w must be a non-empty int8 [out, in] or [experts, out, in] device tensor")
         if out_dtype not in _DTYPES:
