@@ -26,11 +26,12 @@ __device__ __forceinline__ uint64_t order_key(double v) {
 }
 
 // e^x = 2^n e^r, |r| <= ln 2 / 2, by the power series to r^13, whose rest is below r^14 / 14! = 5e-18 of it.
-// 0 below -745, infinity above 709.
+// n ln 2 is taken off in two parts: ln 2 rounded to a multiple of 2^-40, whose product with n < 2^11 is exact, and
+// what that leaves of it.  0 below -745, infinity above 709.
 __device__ __forceinline__ double exp64(double x) {
     x = fmin(fmax(x, -1000.0), 1000.0);
     const double n = rint(x * 1.4426950408889634);
-    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.69314718036912382, x));
+    const double r = fma(n, 0x1.8432a1b0e2634p-43, fma(n, -0x1.62e42fefa4000p-1, x));
     double p = 1.0 / 6227020800.0;
     p = fma(p, r, 1.0 / 479001600.0);
     p = fma(p, r, 1.0 / 39916800.0);
