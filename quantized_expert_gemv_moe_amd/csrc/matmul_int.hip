@@ -6,8 +6,8 @@
 // matrix cores do twice the operations in the same cycles.  Sums stay integers to the
 // end (exact, whatever the order), so a split over K joins without rounding.
 //
-// What bounds them: 8192 x 8192 x 4096 takes 185 to 190 us, 2.9 POP/s, where a library product without an epilogue takes 242:
-// the matrix cores at the power limit (busy for 72 % of the cycles).  1024 tokens, top 8 of 128, 2048 -> 768 gated 83 us, 5.1 TB/s of
+// What bounds them: 8192 x 8192 x 4096 takes 190 us, 2.9 POP/s, and with bias and residual 202, where a library product
+// without an epilogue takes 242 to 267: the matrix cores at the power limit (busy for 72 % of the cycles).  1024 tokens, top 8 of 128, 2048 -> 768 gated 83 us, 5.1 TB/s of
 // weights; 1024 rows of 2048 x 768 gated 9.6 us, 192 tiles of 16 steps with their start and end; 32 tokens of 37 experts,
 // 768 -> 2048, 14.7 us, 4 TB/s: six steps a tile.
 #include "matmul_any.h"

@@ -1,6 +1,6 @@
 """The 128 x 128 tile of the integer products (and the 256 x 256 one, from the same source) rounds a value in the
-same steps wherever it stands: its code holds none of the instructions that round a fused multiply-add straight to fp16, which the compiler takes in some places of a
-tile and not in others."""
+same steps wherever it stands: its code holds none of the instructions that round a fused multiply-add straight
+to fp16, which the compiler takes in some places of a tile and not in others."""
 
 import os
 import re
