@@ -555,8 +555,9 @@ typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
  *   w = s of the chosen, 0 for a masked one; renormalise: divided by their sum (left 0
  *       where that is 0); times scale; rounded once to fp32.
  * A token's ids are -1 and its weights NaN if any unmasked expert's logit is NaN, or
- * +infinity under softmax, or its bias is NaN or +infinity: the planner leaves the
- * token out and the combine makes it NaN.
+ * +infinity under softmax, or its bias is NaN or +infinity, and under softmax also for such a logit
+ * of an expert that only its bias masks, as every score has it in its sum: the planner leaves
+ * the token out and the combine makes it NaN.
  */
 typedef struct {
     int32_t n_experts;   /* 1..MOE_MAX_EXPERTS */

@@ -135,11 +135,13 @@ __device__ __forceinline__ void router_token(const RouterArgs &a, int64_t t, int
         by_logit[q] = l[q] <= a.lowest;
         masked[q] = by_logit[q];
         bool wrong = !(l[q] < INFINITY) && !(a.sigmoid && l[q] == INFINITY);
+        // (a softmax has the logits that only a bias masks in all its scores)
+        const bool everywhere = !a.sigmoid && !by_logit[q] && wrong;
         if constexpr (BIAS) {
             masked[q] = masked[q] || b[q] == -INFINITY;
             wrong = wrong || !(b[q] < INFINITY);
         }
-        bad = bad || (q < n && !masked[q] && wrong);
+        bad = bad || (q < n && (everywhere || (!masked[q] && wrong)));
     }
     bad = __ballot(bad) != 0;
 

@@ -157,3 +157,31 @@ def test_biased_softmax_in_steps_around_the_proof(E, G, keep):
         for renorm in (True, False):
             r = moe.Router(E, k, bias=b, n_groups=G, top_groups=keep, group_score=by, renormalise=renorm)
             compare(logits, "fp32", r, f"steps E={E} G={G} {by}")
+
+
+@pytest.mark.parametrize("E,G,keep", [(24, 1, 1), (256, 8, 3), (512, 16, 5), (600, 1, 1), (640, 32, 7)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_logit_that_only_a_bias_masks(value, E, G, keep):
+    """It is in the sum of every softmax score, so the token has no numbers; a sigmoid's other scores know nothing of it.
+    One that its logit masks as well counts for nothing."""
+    log(f"[case] router masked by bias, logit {value}, {E} {G} {keep}")
+    k, at = 5, E // 2 + 1
+    logits = logits_of(E, 9, E, "fp32")
+    bias = torch.empty(E, device="cuda").normal_(0.0, 0.1, generator=gen(2))
+    bias[at] = -float("inf")
+    other = logits.clone()
+    other[[2, 5], at] = value
+    other[4, at] = -float("inf")
+    for by in ("max", "top2"):
+        for renorm in (True, False):
+            kw = dict(bias=bias, n_groups=G, top_groups=keep, group_score=by, renormalise=renorm)
+            r = moe.Router(E, k, score="sigmoid", **kw)
+            want, got = moe.router_topk(r, logits), moe.router_topk(r, other)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and not bool((got[0] == at).any())
+            r = moe.Router(E, k, score="softmax", **kw)
+            idx, w = moe.router_topk(r, other)
+            torch.cuda.synchronize()
+            assert bool((idx[[2, 5]] == -1).all()) and bool(torch.isnan(w[[2, 5]]).all())
+            rest = [0, 1, 3, 4, 6, 7, 8]
+            compare(other[rest], "fp32", r, f"beside them {by} {renorm}", got=(idx[rest], w[rest]))
