@@ -665,7 +665,8 @@ size_t moe_grouped_int_workspace_size(const moe_linear_int_t *linear, int32_t ma
  *             not.  x of integers takes less: NULL where K is not split, and without room for
  *             a copy rows that are no whole chunks are read where they are.
  * The integer sum is exact; it and the two scales' product are rounded to fp32 once each, and so is
- * what their product and the bias come to (a fused multiply-add).  What follows is as in moe_matmul;
+ * what their product and the bias come to (a fused multiply-add); scales whose product is below
+ * 2^-126 lose bits by it, and one past fp32's range is infinite.  What follows is as in moe_matmul;
  * the last product, of f or of the gate, and a residual's sum may be rounded together.  Repeated
  * calls are bitwise equal.
  */
